@@ -345,6 +345,99 @@ int topk_select(const float *scores, int64_t rows, int64_t cols, int64_t ld,
                 const int32_t *starts, const int32_t *ends, int32_t k, int32_t *out_idx,
                 float *out_val, int32_t *dev_status, sa_stream_t stream);
 
+/* --------------------------------------------------------------------------------------
+ * Serving from a cache: attention of one new token per sequence over a prefix that the
+ * whole batch shares and each sequence's own cache, the attention weight the cached keys
+ * have received, and eviction by that weight.  (The pages have no counterpart; layouts,
+ * head dims and error rules are those above.)
+ * ------------------------------------------------------------------------------------ */
+typedef struct cache_attn_params {
+  const void *q;                  /* bf16 [B][1][HQ][Dqk]: one query token per sequence */
+  const void *k_cache, *v_cache;  /* bf16 [B][S][HK][Dqk], [B][S][HK][Dv]: S is the capacity */
+  const int32_t *lens;            /* device int32 [B]: keys of each sequence, in [0, S] */
+  const void *k_prefix, *v_prefix; /* bf16 [P][HK][Dqk], [P][HK][Dv]; both NULL when P == 0 */
+  void *o;                        /* bf16 [B][1][HQ][Dv] */
+  float *lse;                     /* fp32 [B][HQ][1], natural log */
+  const float *weights;           /* optional fp32 [B][HK][S]: sums so far (NULL: zeros) */
+  float *weights_out;             /* optional fp32 [B][HK][S]; may be `weights` */
+  int32_t B, HQ, HK, Dqk, Dv;
+  int64_t S, P;
+  float softmax_scale;
+  int32_t *dev_status; /* optional device int32 */
+} cache_attn_params;
+
+/*
+ * cache_attn_fwd -- attention of one new token of each sequence b over the P prefix keys
+ * (which every sequence of the batch shares and which are read once for all of them) and
+ * the first lens[b] keys of its own cache.  Query head h uses KV head h / (HQ / HK):
+ *   s_j = scale * q . k_j over both key sets;  lse = ln sum_j exp(s_j);
+ *   o = sum_j exp(s_j - lse) v_j;
+ *   weights_out[b][hk][j] = weights[b][hk][j] + sum_{h in group} exp(s_hj - lse_h) for the
+ *   sequence's own keys j < lens[b] (when weights_out is given), and = weights[b][hk][j]
+ *   (0 without `weights`) behind them.
+ * The new token's own key and value are stored in the cache, and counted in lens, before
+ * the call.  Rows of the caches behind lens[b] are never used, whatever they hold.  A
+ * sequence with no key at all (lens[b] == 0, P == 0) gets o = 0, lse = -inf.  A length
+ * outside [0, S] is clamped to that range and sets SA_STATUS_INDEX in *dev_status.
+ * Supported: HQ / HK <= 128 (SA_ERR_UNSUPPORTED above).  `workspace` is device memory of at
+ * least cache_attn_workspace_size() bytes, 16-byte aligned, not initialised, used by this
+ * call alone until its work has run.  Results do not depend on the order in which CTAs run.
+ */
+int cache_attn_fwd(const cache_attn_params *p, void *workspace, size_t workspace_bytes,
+                   sa_stream_t stream);
+
+/* Bytes of device workspace cache_attn_fwd needs for these shapes (partial outputs and,
+ * with weights_out, the scores of the caches' keys); 0 for invalid sizes. */
+size_t cache_attn_workspace_size(const cache_attn_params *p);
+
+/*
+ * sparse_attn_key_weights -- the attention weight each key has received in a forward pass:
+ *   weights_out[b][hk][j] = weights[b][hk][j] + sum_{h in group} sum_{i: j in A_i}
+ *   exp(scale * q_ih . k_j - lse_ih)
+ * (weights NULL: zeros).  Takes the q, k, softmax_scale, sparse lists (every mode) and
+ * dev_status of `p` and the lse that sparse_attn_fwd wrote; v, o and the gradient fields are
+ * not read (Dv still selects the head-dim pair).  A query whose lse is -inf adds nothing.
+ *   weights, weights_out  fp32 [B][HK][Sk]; may be the same array.
+ * The sums are taken in a fixed order (two calls give identical bits).  `workspace`: device
+ * memory of at least sparse_attn_key_weights_workspace_size() bytes (which may be 0),
+ * 16-byte aligned, not initialised.
+ */
+int sparse_attn_key_weights(const sparse_attn_params *p, const float *weights,
+                            float *weights_out, void *workspace, size_t workspace_bytes,
+                            sa_stream_t stream);
+size_t sparse_attn_key_weights_workspace_size(const sparse_attn_params *p);
+
+typedef struct cache_evict_params {
+  const void *k_cache, *v_cache;  /* bf16 [B][S][HK][Dqk], [B][S][HK][Dv] */
+  const float *weights;           /* fp32 [B][HK][S]: the weight each key has received */
+  const int32_t *lens;            /* device int32 [B], in [0, S] */
+  void *k_out, *v_out;            /* bf16 [B][S_out][HK][Dqk], [B][S_out][HK][Dv] */
+  float *weights_out;             /* fp32 [B][HK][S_out] */
+  int32_t *lens_out;              /* device int32 [B] */
+  int32_t *keep;                  /* device int32 [B][HK][budget] */
+  int32_t B, HK, Dqk, Dv;
+  int64_t S, S_out;
+  int32_t budget, sinks, recent;
+  int32_t *dev_status;            /* optional device int32 */
+} cache_evict_params;
+
+/*
+ * cache_evict -- cuts every sequence's cache to at most `budget` keys per KV head.  A
+ * sequence of n = lens[b] > budget keys keeps, per KV head, its first `sinks` keys, its last
+ * `recent` keys and the budget - sinks - recent keys between them with the largest weight
+ * (ties to the smaller position, -0 equals +0, NaN ranks above +inf); a shorter one keeps all.
+ *   keep[b][hk]      the kept positions, ascending, then -1;
+ *   k_out, v_out     rows i < lens_out[b]: the kept rows in that order; later rows are left
+ *                    as they were;
+ *   weights_out      the kept keys' weights, then zeros up to S_out (what tokens appended
+ *                    later start from);
+ *   lens_out[b]      min(lens[b], budget).
+ * The outputs must not overlap the inputs (SA_ERR_INVALID for equal base pointers).
+ * 1 <= budget <= S_out, sinks, recent >= 0, sinks + recent <= budget.  A length outside
+ * [0, S] is clamped and sets SA_STATUS_INDEX in *dev_status.  Needs no workspace.
+ */
+int cache_evict(const cache_evict_params *p, sa_stream_t stream);
+
 /* Static description of an SA_* code. */
 const char *sparse_attn_error_string(int code);
 

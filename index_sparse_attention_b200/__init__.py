@@ -17,6 +17,8 @@ from ._lib import SA_MODE_BLOCK, SA_MODE_DENSE, SA_MODE_INDEX, SA_TILE, SparseAt
 __all__ = ["BlockSparse", "block_mask_to_block_sparse", "index_to_block_sparse",
            "sparse_attn_fwd", "sparse_attn_fwd_gather", "sparse_attn_bwd",
            "sparse_attn_bwd_workspace_size", "sparse_attn_bwd_noalloc", "topk_select",
+           "cache_attn_fwd", "cache_attn_workspace_size", "sparse_attn_key_weights",
+           "cache_evict",
            "sparse_attn_set_wait_limit_ns", "sparse_attn_set_forward_form",
            "sparse_attn_set_backward_form", "SparseAttnError", "SA_TILE"]
 
@@ -313,6 +315,201 @@ def topk_select(scores, k, starts=None, ends=None, with_values=False, out_idx=No
                              k, _ptr(out_idx), _ptr(out_val), _ptr(dev_status),
                              _stream(scores.device)))
     return (out_idx, out_val) if with_values else out_idx
+
+
+def _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, weights, weights_out, o,
+                  lse, dev_status):
+    _check("q", q, torch.bfloat16, ndim=4)
+    B, T, HQ, Dqk = q.shape
+    _require(T == 1, f"q must hold one token per sequence [B, 1, HQ, Dqk], got {tuple(q.shape)}")
+    dev = q.device
+    _check("k_cache", k_cache, torch.bfloat16, ndim=4, device=dev)
+    _check("v_cache", v_cache, torch.bfloat16, ndim=4, device=dev)
+    S, HK, Dv = k_cache.shape[1], k_cache.shape[2], v_cache.shape[3]
+    _require(k_cache.shape[0] == B and k_cache.shape[3] == Dqk,
+             f"k_cache must be [B={B}, S, HK, Dqk={Dqk}], got {tuple(k_cache.shape)}")
+    _require(tuple(v_cache.shape[:3]) == (B, S, HK),
+             f"v_cache must be [B, S, HK, Dv] with k_cache's first three sizes {(B, S, HK)}, "
+             f"got {tuple(v_cache.shape)}")
+    _check("lens", lens, torch.int32, shape=(B,), device=dev)
+    _require((k_prefix is None) == (v_prefix is None), "k_prefix and v_prefix go together")
+    P = 0
+    if k_prefix is not None:
+        _check("k_prefix", k_prefix, torch.bfloat16, ndim=3, device=dev)
+        P = k_prefix.shape[0]
+        _check("k_prefix", k_prefix, torch.bfloat16, shape=(P, HK, Dqk), device=dev)
+        _check("v_prefix", v_prefix, torch.bfloat16, shape=(P, HK, Dv), device=dev)
+        if P == 0:
+            k_prefix = v_prefix = None
+    for name, t in (("weights", weights), ("weights_out", weights_out)):
+        if t is not None:
+            _check(name, t, torch.float32, shape=(B, HK, S), device=dev)
+    if o is not None:
+        _check("o", o, torch.bfloat16, shape=(B, 1, HQ, Dv), device=dev)
+    if lse is not None:
+        _check("lse", lse, torch.float32, shape=(B, HQ, 1), device=dev)
+    _check_status(dev_status, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dqk)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return _lib.CacheAttnStruct(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), ptr(k_prefix),
+        ptr(v_prefix), ptr(o), ptr(lse), ptr(weights), ptr(weights_out), B, HQ, HK, Dqk, Dv, S, P,
+        float(scale), ptr(dev_status))
+
+
+@_on_device("q")
+def cache_attn_workspace_size(q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None,
+                              with_weights=False):
+    """Bytes of device workspace cache_attn_fwd needs for these shapes."""
+    L = _lib.load()
+    p = _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, None, None, None, None, None,
+                      None)
+    p.weights_out = 16 if with_weights else None  # (only whether it is given matters)
+    return int(L.cache_attn_workspace_size(ctypes.byref(p)))
+
+
+@_on_device("q")
+def cache_attn_fwd(q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None, softmax_scale=None,
+                   weights=None, with_weights=False, weights_out=None, o=None, lse=None,
+                   workspace=None, dev_status=None):
+    """O [B,1,HQ,Dv] (bf16) and LSE [B,HQ,1] (fp32) of one new token per sequence over the
+    prefix k_prefix / v_prefix [P,HK,D] that the batch shares (read once for all sequences)
+    and the first lens[b] (int32 [B]) keys of each sequence's cache k_cache / v_cache
+    [B,S,HK,D].
+
+    With ``with_weights`` (or a ``weights_out``) also weights_out [B,HK,S] (fp32):
+    ``weights`` (zeros when omitted) plus the attention weight that each of the sequence's
+    own keys gets from this token, summed over the group's query heads; ``weights_out`` may
+    be ``weights`` itself, which adds in place."""
+    L = _lib.load()
+    p = _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, softmax_scale, weights,
+                      weights_out, o, lse, dev_status)
+    _require(weights is None or with_weights or weights_out is not None,
+             "weights needs with_weights or a weights_out")
+    if o is None:
+        o = torch.empty((p.B, 1, p.HQ, p.Dv), dtype=torch.bfloat16, device=q.device)
+        p.o = o.data_ptr()
+    if lse is None:
+        lse = torch.empty((p.B, p.HQ, 1), dtype=torch.float32, device=q.device)
+        p.lse = lse.data_ptr()
+    if with_weights and weights_out is None:
+        weights_out = torch.empty((p.B, p.HK, p.S), dtype=torch.float32, device=q.device)
+        p.weights_out = weights_out.data_ptr()
+    if workspace is None:
+        need = int(L.cache_attn_workspace_size(ctypes.byref(p)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check("workspace", workspace, torch.uint8, device=q.device)
+    _lib.check("cache_attn_fwd", L.cache_attn_fwd(ctypes.byref(p), _ptr(workspace),
+                                                  workspace.numel(), _stream(q.device)))
+    return (o, lse) if weights_out is None else (o, lse, weights_out)
+
+
+@_on_device("q")
+def sparse_attn_key_weights(q, k, lse, sparse, softmax_scale=None, weights=None, weights_out=None,
+                            workspace=None, dev_status=None):
+    """The attention weight each key received in a forward pass, fp32 [B,HK,Sk]: the sum
+    over the group's query heads and all queries that see the key of exp(scale q.k - lse),
+    with the lse [B,HQ,Sq] that sparse_attn_fwd returned for the same q, k, lists and scale.
+    Added to ``weights`` when given; ``weights_out`` may be ``weights`` itself."""
+    L = _lib.load()
+    _check("q", q, torch.bfloat16, ndim=4)
+    B, Sq, HQ, Dqk = q.shape
+    dev = q.device
+    _check("k", k, torch.bfloat16, ndim=4, device=dev)
+    _require(k.shape[0] == B and k.shape[3] == Dqk,
+             f"k must be [B={B}, Sk, HK, Dqk={Dqk}], got {tuple(k.shape)}")
+    Sk, HK = k.shape[1], k.shape[2]
+    _check("lse", lse, torch.float32, shape=(B, HQ, Sq), device=dev)
+    _require(isinstance(sparse, BlockSparse), "sparse must be a BlockSparse", TypeError)
+    for name, t in (("weights", weights), ("weights_out", weights_out)):
+        if t is not None:
+            _check(name, t, torch.float32, shape=(B, HK, Sk), device=dev)
+    _check_status(dev_status, dev)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(Dqk)
+    if weights_out is None:
+        weights_out = torch.empty((B, HK, Sk), dtype=torch.float32, device=dev)
+    Dv = {64: 64, 128: 128, 192: 128, 256: 256}.get(Dqk, Dqk)  # (not read; selects the pair)
+    p = _lib.ParamsStruct(
+        q.data_ptr(), k.data_ptr(), None, None, lse.data_ptr(), None, None, None, None, B, HQ, HK,
+        Dqk, Dv, Sq, Sk, float(softmax_scale), ctypes.pointer(sparse.c),
+        None if dev_status is None else dev_status.data_ptr())
+    if workspace is None:
+        need = int(L.sparse_attn_key_weights_workspace_size(ctypes.byref(p)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check("workspace", workspace, torch.uint8, device=dev)
+    _lib.check("sparse_attn_key_weights",
+               L.sparse_attn_key_weights(ctypes.byref(p), _ptr(weights), _ptr(weights_out),
+                                         _ptr(workspace), workspace.numel(), _stream(dev)))
+    return weights_out
+
+
+@_on_device("k_cache")
+def cache_evict(k_cache, v_cache, weights, lens, budget, sinks=0, recent=0, k_out=None, v_out=None,
+                weights_out=None, lens_out=None, keep=None, dev_status=None):
+    """Cuts every sequence's cache to at most ``budget`` keys per KV head: its first
+    ``sinks`` keys, its last ``recent`` keys and the heaviest of the keys between them by
+    ``weights`` [B,HK,S] (ties to the smaller position), in their order.
+
+    Returns k_out, v_out [B,S_out,HK,D] (rows behind the kept ones left as they were; S_out
+    is the capacity of a given k_out, else that of k_cache), weights_out [B,HK,S_out] (zeros
+    behind the kept keys), lens_out int32 [B] and keep int32 [B,HK,budget] (the kept
+    positions, then -1).  The outputs must not overlap the inputs."""
+    L = _lib.load()
+    _check("k_cache", k_cache, torch.bfloat16, ndim=4)
+    B, S, HK, Dqk = k_cache.shape
+    dev = k_cache.device
+    _check("v_cache", v_cache, torch.bfloat16, ndim=4, device=dev)
+    Dv = v_cache.shape[3]
+    _check("v_cache", v_cache, torch.bfloat16, shape=(B, S, HK, Dv), device=dev)
+    _check("weights", weights, torch.float32, shape=(B, HK, S), device=dev)
+    _check("lens", lens, torch.int32, shape=(B,), device=dev)
+    _check_status(dev_status, dev)
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    if k_out is None:
+        S_out = S if v_out is None else v_out.shape[1]
+        k_out = torch.empty((B, S_out, HK, Dqk), dtype=torch.bfloat16, device=dev)
+    _check("k_out", k_out, torch.bfloat16, ndim=4, device=dev)
+    S_out = k_out.shape[1]
+    _check("k_out", k_out, torch.bfloat16, shape=(B, S_out, HK, Dqk), device=dev)
+    _require(1 <= budget <= S_out, f"budget must be in [1, {S_out}] (k_out's rows), got {budget}")
+    _require(sinks >= 0 and recent >= 0 and sinks + recent <= budget,
+             f"sinks and recent must be non-negative with a sum of at most budget={budget}, "
+             f"got {sinks} and {recent}")
+    if v_out is None:
+        v_out = torch.empty((B, S_out, HK, Dv), dtype=torch.bfloat16, device=dev)
+    _check("v_out", v_out, torch.bfloat16, shape=(B, S_out, HK, Dv), device=dev)
+    if weights_out is None:
+        weights_out = torch.empty((B, HK, S_out), dtype=torch.float32, device=dev)
+    _check("weights_out", weights_out, torch.float32, shape=(B, HK, S_out), device=dev)
+    if lens_out is None:
+        lens_out = torch.empty((B,), dtype=torch.int32, device=dev)
+    _check("lens_out", lens_out, torch.int32, shape=(B,), device=dev)
+    if keep is None:
+        keep = torch.empty((B, HK, budget), dtype=torch.int32, device=dev)
+    _check("keep", keep, torch.int32, shape=(B, HK, budget), device=dev)
+    _require_apart((k_cache, v_cache, weights, lens), (k_out, v_out, weights_out, lens_out, keep))
+    p = _lib.CacheEvictStruct(
+        k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), lens.data_ptr(),
+        k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(), lens_out.data_ptr(),
+        keep.data_ptr(), B, HK, Dqk, Dv, S, S_out, budget, sinks, recent,
+        None if dev_status is None else dev_status.data_ptr())
+    _lib.check("cache_evict", L.cache_evict(ctypes.byref(p), _stream(dev)))
+    return k_out, v_out, weights_out, lens_out, keep
+
+
+def _require_apart(inputs, outputs):
+    """No output shares memory with an input or with another output."""
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+    taken = [span(t) for t in inputs]
+    for t in outputs:
+        lo, hi = span(t)
+        _require(all(hi <= a or b <= lo for a, b in taken),
+                 "an output overlaps an input or another output")
+        taken.append((lo, hi))
 
 
 def sparse_attn_set_wait_limit_ns(ns):

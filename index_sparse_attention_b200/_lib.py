@@ -49,6 +49,11 @@ EXPORTS = (
     "sparse_attn_set_backward_form",
     "sparse_attn_error_string",
     "topk_select",
+    "cache_attn_fwd",
+    "cache_attn_workspace_size",
+    "sparse_attn_key_weights",
+    "sparse_attn_key_weights_workspace_size",
+    "cache_evict",
 )
 
 
@@ -71,6 +76,32 @@ class ParamsStruct(ctypes.Structure):
         ("Dqk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("Sq", ctypes.c_int64),
         ("Sk", ctypes.c_int64), ("softmax_scale", ctypes.c_float),
         ("sparse", ctypes.POINTER(BlockSparseStruct)), ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class CacheAttnStruct(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p), ("k_prefix", ctypes.c_void_p), ("v_prefix", ctypes.c_void_p),
+        ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+        ("weights_out", ctypes.c_void_p),
+        ("B", ctypes.c_int32), ("HQ", ctypes.c_int32), ("HK", ctypes.c_int32),
+        ("Dqk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("S", ctypes.c_int64),
+        ("P", ctypes.c_int64), ("softmax_scale", ctypes.c_float),
+        ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class CacheEvictStruct(ctypes.Structure):
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p),
+        ("weights_out", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
+        ("keep", ctypes.c_void_p),
+        ("B", ctypes.c_int32), ("HK", ctypes.c_int32), ("Dqk", ctypes.c_int32),
+        ("Dv", ctypes.c_int32), ("S", ctypes.c_int64), ("S_out", ctypes.c_int64),
+        ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32),
+        ("dev_status", ctypes.c_void_p),
     ]
 
 
@@ -114,6 +145,17 @@ def load():
     i64 = ctypes.c_int64
     L.topk_select.argtypes = [vp, i64, i64, i64, vp, vp, ctypes.c_int32, vp, vp, vp, vp]
     L.topk_select.restype = ctypes.c_int
+    P_ca, P_ce = ctypes.POINTER(CacheAttnStruct), ctypes.POINTER(CacheEvictStruct)
+    L.cache_attn_fwd.argtypes = [P_ca, vp, ctypes.c_size_t, vp]
+    L.cache_attn_fwd.restype = ctypes.c_int
+    L.cache_attn_workspace_size.argtypes = [P_ca]
+    L.cache_attn_workspace_size.restype = ctypes.c_size_t
+    L.sparse_attn_key_weights.argtypes = [P_p, vp, vp, vp, ctypes.c_size_t, vp]
+    L.sparse_attn_key_weights.restype = ctypes.c_int
+    L.sparse_attn_key_weights_workspace_size.argtypes = [P_p]
+    L.sparse_attn_key_weights_workspace_size.restype = ctypes.c_size_t
+    L.cache_evict.argtypes = [P_ce, vp]
+    L.cache_evict.restype = ctypes.c_int
     L.sparse_attn_error_string.argtypes = [ctypes.c_int]
     L.sparse_attn_error_string.restype = ctypes.c_char_p
     _lib = L

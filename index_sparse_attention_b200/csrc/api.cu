@@ -42,21 +42,27 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 4-D map over a [B][S][H][D] bf16 tensor with 64 x box_rows (D x S) boxes, 128-byte
-// swizzle.  Out-of-range rows (and columns) read as zeros.
-bool make_map(CUtensorMap* m, const void* base, int D, int64_t S, int H, int B, int box_rows) {
+}  // namespace
+
+namespace sa {
+bool make_map(CUtensorMap* m, const void* base, int D, int64_t S, int H, int B, int box_rows,
+              int box_heads) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(S),
                         static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(B)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(H) * D * 2, static_cast<cuuint64_t>(D) * 2,
                            static_cast<cuuint64_t>(S) * H * D * 2};
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_heads),
+                       1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+}  // namespace sa
+
+namespace {
 
 // 4-D map over the fp32 dQ accumulator [B][Sq][HQ][D] with 64 x 32 (D x S) boxes, no
 // swizzle: the target of the backward's bulk reduce-adds.
@@ -81,6 +87,9 @@ bool dims_supported(int dqk, int dv) {
          (dqk == 256 && dv == 256);
 }
 
+}  // namespace
+
+namespace sa {
 int fill_args(const sparse_attn_params* p, AttnArgs* a, bool backward) {
   if (!p || !p->sparse) return SA_ERR_INVALID;
   const sa_block_sparse* s = p->sparse;
@@ -143,6 +152,9 @@ int fill_args(const sparse_attn_params* p, AttnArgs* a, bool backward) {
   a->wait_limit_ns = lim ? lim : kWaitLimitNs;
   return SA_OK;
 }
+}  // namespace sa
+
+namespace {
 
 // Forward: Q in 128-row boxes, K also in 64-row boxes (CTA pairs load half tiles).
 // Backward: Q and dO in 64-row boxes (the backward consumes query tiles in 64-row

@@ -87,6 +87,15 @@ inline int once_per_device(PerDeviceOnce& o, F&& set) {
   return rc;
 }
 
+// 4-D tensor map over a [B][S][H][D] bf16 tensor (dimension order D, S, H, B) with
+// 64 x box_rows x box_heads (D x S x H) boxes, 128-byte swizzle.  Out-of-range rows (and
+// columns) read as zeros.
+bool make_map(CUtensorMap* m, const void* base, int D, int64_t S, int H, int B, int box_rows,
+              int box_heads = 1);
+
+// Checks an attention call's parameters and fills the launch arguments from them.
+int fill_args(const sparse_attn_params* p, AttnArgs* a, bool backward);
+
 // Every kernel is launched on the current device.  A stream created on another device
 // is refused with SA_ERR_DEVICE before anything is enqueued (the legacy and per-thread
 // default streams always belong to the current device).
@@ -94,6 +103,11 @@ inline int check_stream_device(cudaStream_t st) {
   int cur = -1;
   if (cudaGetDevice(&cur) != cudaSuccess) return SA_ERR_CUDA;
   if (st == nullptr || st == cudaStreamLegacy || st == cudaStreamPerThread) return SA_OK;
+  // A stream that is being captured cannot be asked for its device (the query would end the
+  // capture); a launch into a capture of another device's stream fails by itself.
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone)
+    return SA_OK;
   int sd = -1;
   if (cudaStreamGetDevice(st, &sd) != cudaSuccess) return SA_ERR_CUDA;
   return sd == cur ? SA_OK : SA_ERR_DEVICE;
