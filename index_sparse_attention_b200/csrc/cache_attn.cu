@@ -7,117 +7,400 @@
 // lse = m' + ln l', o = o' / l'.
 // Three launches: the parts (this file's main kernel, work split as in cache_plan.cuh), their
 // join, and, when asked for, the keys' weights from the stored scores.
+#include <type_traits>
+
 #include "cache_plan.cuh"
 #include "sa_kernels.h"
 
 namespace sa {
 namespace cache {
 
-constexpr int kSimple = 256;  // threads of the main kernel
-constexpr int kRowBlk = 8;
+template <int DQK, int DV>
+struct Cfg {
+  static constexpr int kN = DQK <= 128 ? 128 : 64;  // keys of a tile
+  static constexpr int kQStages = DQK == 256 ? 1 : 2;
+  static constexpr int kKStages = DQK == 64 ? 5 : 3;
+  static constexpr int kVStages = DQK == 64 ? 5 : DQK == 192 ? 3 : 2;
+  static constexpr int kQPanel = 128 * 128;  // 64 columns x 128 rows
+  static constexpr int kKPanel = kN * 128;   // 64 columns x kN rows (V too)
+  static constexpr int kQBytes = 128 * DQK * 2;
+  static constexpr int kKBytes = kN * DQK * 2;
+  static constexpr int kVBytes = kN * DV * 2;
+  static constexpr int kKOff = kQStages * kQBytes;
+  static constexpr int kVOff = kKOff + kKStages * kKBytes;
+  // what the two warps of a quarter exchange, [2][128]: a tile's row maxima, a part's row sums
+  // (a barrier of the pair lies between one use's reads and the next one's writes)
+  static constexpr int kXOff = kVOff + kVStages * kVBytes;
+  static constexpr int kFindOff = kXOff + 1024;
+  static constexpr int kBarOff = kFindOff + 66 * 8;
+  static constexpr int kSmem = kBarOff + 256 + 1024;
+  static constexpr int kThreads = 352;
+  static constexpr uint32_t kOCol = 256;  // S / P buffers at columns 0 and 128
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(kKStages <= 5 && kVStages <= 5, "barrier slots");
+};
+
+enum : int { kBQF = 0, kBQE = 2, kBKF = 4, kBKE = 9, kBVF = 14, kBVE = 19, kBSF = 24, kBPF = 26,
+             kBOD = 28, kBDrain = 29, kNumBars = 30 };
+
+// maps: Q for prefix row tiles and for one sequence, K / V of the prefix and of the caches
+struct Maps {
+  CUtensorMap qp, qc, kp, vp, kc, vc;
+};
 
 template <int DQK, int DV>
-__global__ void __launch_bounds__(kSimple) cache_part_kernel(const Args a) {
-  __shared__ int64_t sh[66];
-  __shared__ float qs[kRowBlk][DQK];
-  __shared__ float ss[kRowBlk][128];
-  __shared__ float mrow[kRowBlk], lrow[kRowBlk], arow[kRowBlk];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = blockIdx.x;
-  const Found f = find_range<kSimple>(a, c, sh);
-  if (c == 0)
-    for (int b = tid; b < a.B; b += kSimple) {
-      const int n = __ldg(a.lens + b);
-      if (n < 0 || n > a.S) report_status(a.status, kStatusIndex);
+__global__ void __launch_bounds__(352, 1)
+    cache_part_kernel(const __grid_constant__ Maps maps, const Args a) {
+  using C = Cfg<DQK, DV>;
+  constexpr int kN = C::kN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * kNumBars);
+  volatile WaitCtl* ctl =
+      reinterpret_cast<volatile WaitCtl*>(smem + C::kBarOff + 8 * kNumBars + 4);
+  auto BAR = [&](int k) { return sbase + C::kBarOff + 8u * static_cast<uint32_t>(k); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kNumBars; ++k) mbar_init(BAR(k), k == kBPF || k == kBPF + 1 ? 256 : 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const Found f = find_range<C::kThreads>(
+      a, cta, reinterpret_cast<int64_t*>(smem + C::kFindOff));  // (ends with a barrier)
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  const int n_iter = static_cast<int>(f.u1 - f.u0);
+  Walk w{};
+  if (n_iter > 0) w.init(a, f.u0, f.b, f.off);
+  int issued_k = 0, issued_v = 0, issued_q = 0;  // loads issued (the abort path drains the last)
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- Q and K producer
+    if (cta == 0)  // lengths out of range are reported once
+      for (int b = lane; b < a.B; b += 32) {
+        const int n = __ldg(a.lens + b);
+        if (n < 0 || n > a.S) report_status(a.status, kStatusIndex);
+      }
+    bool first = true;
+    for (int it = 0; it < n_iter; ++it) {
+      const int ks = it % C::kKStages, ku = it / C::kKStages;
+      if (!warp_wait(BAR(kBKE + ks), (ku & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(BAR(kBKF + ks), C::kKBytes);
+        const int k0 = static_cast<int>(w.tile) * kN;
+        for (int c = 0; c < DQK / 64; ++c)
+          tma_load_4d(sbase + C::kKOff + ks * C::kKBytes + c * C::kKPanel,
+                      w.prefix ? &maps.kp : &maps.kc, BAR(kBKF + ks), c * 64, k0, w.hk,
+                      w.prefix ? 0 : w.b);
+      }
+      __syncwarp();
+      issued_k = it + 1;
+      if (first) {
+        const int qs = issued_q % C::kQStages, qu = issued_q / C::kQStages;
+        if (!warp_wait(BAR(kBQE + qs), (qu & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
+        if (elect_one()) {
+          const int rep = w.prefix ? a.rep_p : a.rep_c, rows = w.prefix ? a.rows_p : a.rows_c;
+          mbar_arrive_expect_tx(BAR(kBQF + qs), rep * rows * DQK * 2);
+          for (int r = 0; r < rep; ++r)
+            for (int c = 0; c < DQK / 64; ++c)
+              tma_load_4d(sbase + qs * C::kQBytes + c * C::kQPanel + r * 32 * 128,
+                          w.prefix ? &maps.qp : &maps.qc, BAR(kBQF + qs), c * 64,
+                          w.prefix ? w.rt * a.nb : w.b, w.hk * a.G, 0);
+        }
+        __syncwarp();
+        ++issued_q;
+      }
+      if (it + 1 < n_iter) first = w.next(a);
     }
-  Walk w;
-  if (f.u0 < f.u1) w.init(a, f.u0, f.b, f.off);
-  int64_t u = f.u0;
-  while (u < f.u1) {
-    const int64_t n_tiles = min64(w.tiles - w.tile, f.u1 - u);
-    const int rows = w.prefix ? a.nb * a.G : a.G;
-    const int64_t slot = w.seg + c;
-    for (int r0 = 0; r0 < rows; r0 += kRowBlk) {
-      __syncthreads();
-      for (int e = tid; e < kRowBlk * DQK; e += kSimple) {
-        const int r = r0 + e / DQK, d = e % DQK;
-        float x = 0.f;
-        if (r < rows) {
-          const int g = w.prefix ? r / a.nb : r;
-          const int b = w.prefix ? w.rt * a.nb + r % a.nb : w.b;
-          if (b < a.B)
-            x = __bfloat162float(a.q[(static_cast<int64_t>(b) * a.HQ + w.hk * a.G + g) * DQK + d]);
-        }
-        qs[e / DQK][d] = x;
+    // every arrival on the stages' barriers has landed before the CTA may leave
+    if (issued_k == n_iter) {
+      for (int it = max(0, n_iter - C::kKStages); it < n_iter; ++it)
+        if (!warp_wait(BAR(kBKE + it % C::kKStages), (it / C::kKStages) & 1, ctl, a.status,
+                       a.wait_limit_ns))
+          break;
+      for (int q = max(0, issued_q - C::kQStages); q < issued_q; ++q)
+        if (!warp_wait(BAR(kBQE + q % C::kQStages), (q / C::kQStages) & 1, ctl, a.status,
+                       a.wait_limit_ns))
+          break;
+    }
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- V producer
+    for (int it = 0; it < n_iter; ++it) {
+      const int vs = it % C::kVStages, vu = it / C::kVStages;
+      if (!warp_wait(BAR(kBVE + vs), (vu & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(BAR(kBVF + vs), C::kVBytes);
+        const int k0 = static_cast<int>(w.tile) * kN;
+        for (int c = 0; c < DV / 64; ++c)
+          tma_load_4d(sbase + C::kVOff + vs * C::kVBytes + c * C::kKPanel,
+                      w.prefix ? &maps.vp : &maps.vc, BAR(kBVF + vs), c * 64, k0, w.hk,
+                      w.prefix ? 0 : w.b);
       }
-      if (tid < kRowBlk) {
-        mrow[tid] = -INFINITY;
-        lrow[tid] = 0.f;
+      __syncwarp();
+      issued_v = it + 1;
+      if (it + 1 < n_iter) w.next(a);
+    }
+    if (issued_v == n_iter)
+      for (int it = max(0, n_iter - C::kVStages); it < n_iter; ++it)
+        if (!warp_wait(BAR(kBVE + it % C::kVStages), (it / C::kVStages) & 1, ctl, a.status,
+                       a.wait_limit_ns))
+          break;
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_s = idesc_bf16(128, kN, 0, 0);
+    constexpr uint32_t idesc_o = idesc_bf16(128, DV, 0, 1);
+    int part = 0;                 // part of the S being issued
+    bool first_s = true, first_o = true;
+    Walk wo = w;                  // the walk of the P V being issued (one tile behind)
+    auto issue_s = [&](int it) -> bool {
+      const int ks = it % C::kKStages, ku = it / C::kKStages;
+      const int qs = part % C::kQStages, qu = part / C::kQStages;
+      if (first_s && !warp_wait(BAR(kBQF + qs), qu & 1, ctl, a.status, a.wait_limit_ns)) return false;
+      if (!warp_wait(BAR(kBKF + ks), ku & 1, ctl, a.status, a.wait_limit_ns)) return false;
+      tc_fence_after();
+      const bool more = it + 1 < n_iter;
+      const bool ends = !more || w.next(a);  // the part's last tile
+      const uint64_t kd = sw128_desc(sbase + C::kKOff + ks * C::kKBytes, 16, 1024);
+      const uint64_t qd = sw128_desc(sbase + qs * C::kQBytes, 16, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < DQK / 16; ++kk)
+          umma_ss(tmem + (it & 1) * 128, qd + (((kk >> 2) * C::kQPanel + (kk & 3) * 32) >> 4),
+                  kd + (((kk >> 2) * C::kKPanel + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit(BAR(kBSF + (it & 1)));
+        umma_commit(BAR(kBKE + ks));
+        if (ends) umma_commit(BAR(kBQE + qs));
       }
-      float acc[kRowBlk];
-      for (int r = 0; r < kRowBlk; ++r) acc[r] = 0.f;
-      for (int64_t t = w.tile; t < w.tile + n_tiles; ++t) {
-        const int64_t k0 = t * a.kn;
-        const int nk = static_cast<int>(min64(a.kn, w.keys - k0));
-        const int64_t row0 = w.prefix ? k0 : static_cast<int64_t>(w.b) * a.S + k0;
-        const __nv_bfloat16* kb = (w.prefix ? a.kp : a.k) + (row0 * a.HK + w.hk) * DQK;
-        const __nv_bfloat16* vb = (w.prefix ? a.vp : a.v) + (row0 * a.HK + w.hk) * DV;
-        __syncthreads();
-        for (int e = tid; e < kRowBlk * 128; e += kSimple) {
-          const int r = e / 128, j = e % 128;
-          float x = -INFINITY;
-          if (j < nk) {
-            x = 0.f;
-            const __nv_bfloat16* kr = kb + static_cast<int64_t>(j) * a.HK * DQK;
-            for (int d = 0; d < DQK; ++d) x = fmaf(qs[r][d], __bfloat162float(kr[d]), x);
-            x *= a.scale_log2;
-            if (!w.prefix && a.scores && r0 + r < a.G)
-              a.scores[(static_cast<int64_t>(w.b) * a.HQ + w.hk * a.G + r0 + r) * a.Sp + k0 + j] = x;
+      __syncwarp();
+      first_s = ends;
+      if (ends) ++part;
+      return true;
+    };
+    bool ok = n_iter > 0 && issue_s(0);
+    for (int it = 0; ok && it < n_iter; ++it) {
+      if (it + 1 < n_iter && !issue_s(it + 1)) break;
+      const int vs = it % C::kVStages, vu = it / C::kVStages;
+      if (!warp_wait(BAR(kBPF + (it & 1)), (it >> 1) & 1, ctl, a.status, a.wait_limit_ns)) break;
+      if (!warp_wait(BAR(kBVF + vs), vu & 1, ctl, a.status, a.wait_limit_ns)) break;
+      tc_fence_after();
+      const uint64_t vd = sw128_desc(sbase + C::kVOff + vs * C::kVBytes, C::kKPanel, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)
+          umma_ts(tmem + C::kOCol, tmem + (it & 1) * 128 + kk * 8, vd + ((kk * 2048) >> 4), idesc_o,
+                  (!first_o || kk > 0) ? 1u : 0u);
+        umma_commit(BAR(kBOD));
+        umma_commit(BAR(kBVE + vs));
+      }
+      __syncwarp();
+      if (it + 1 < n_iter) first_o = wo.next(a);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int quarter = warp & 3, hc = (warp - 2) >> 2;
+    const int pair_bar = 1 + quarter;  // the two warps of a TMEM lane quarter
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* xch = reinterpret_cast<float*>(smem + C::kXOff);
+    const int r = quarter * 32 + lane;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool first = true;
+    auto both = [&](bool v) { return named_bar_and(pair_bar, 64, v); };
+    // One tile: S columns [c0, c0 + NC) of this thread's row -> P.  kRep: the row's copy in
+    // this quarter takes the quarter's kN / 4 columns, the others' P is zero.
+    auto tile = [&](auto nc, bool rep, int it, bool active) -> bool {
+      constexpr int NC = decltype(nc)::value;
+      const int sb = it & 1;
+      const uint32_t scol = tl + sb * 128;
+      const int c0 = rep ? quarter * (kN / 4) + hc * NC : hc * NC;
+      const int k0 = static_cast<int>(w.tile) * kN;
+      const int lim = static_cast<int>(min64(kN, w.keys - k0));
+      if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBSF + sb), (it >> 1) & 1, ctl, a.status,
+                                                  a.wait_limit_ns))))
+        return false;
+      tc_fence_after();
+      uint32_t u[NC];
+      if constexpr (NC >= 32) {
+#pragma unroll
+        for (int j = 0; j < NC / 32; ++j) tmem_ld32(scol + c0 + 32 * j, u + 32 * j);
+      } else if constexpr (NC == 16) {
+        tmem_ld16(scol + c0, u);
+      } else {
+        tmem_ld8(scol + c0, u);
+      }
+      tmem_wait_ld();
+      float x[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(u[c]) * a.scale_log2;
+      if (lim < kN) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (c0 + c >= lim) x[c] = -INFINITY;
+      }
+      if (a.scores && !w.prefix && active) {
+        const int g = rep ? lane : r;
+        float4* dst = reinterpret_cast<float4*>(
+            a.scores + (static_cast<int64_t>(w.b) * a.HQ + w.hk * a.G + g) * a.Sp + k0 + c0);
+#pragma unroll
+        for (int e = 0; e < NC / 4; ++e)
+          dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+      }
+      float mx4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int c = 4; c < NC; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], x[c]);
+      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      xch[hc * 128 + r] = mx;
+      // both warps have read their S columns past this barrier: P may be written over them
+      named_bar_sync(pair_bar, 64);
+      mx = fmaxf(xch[r], xch[128 + r]);
+      const bool need = active && mx > m_run + 8.0f;
+      const float alpha = need ? ex2(m_run - mx) : 1.f;
+      if (__any_sync(0xFFFFFFFFu, need)) {
+        if (!first) {  // O holds P V up to the tile before: rescale this warp's O columns
+          if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), (it - 1) & 1, ctl, a.status,
+                                                      a.wait_limit_ns))))
+            return false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tl + C::kOCol + c, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st32(tl + C::kOCol + c, ov);
           }
-          ss[r][j] = x;
+          tmem_wait_st();
         }
-        __syncthreads();
-        {  // warp r: the row's max and sum
-          const int r = warp;
-          float mx = mrow[r];
-          for (int j = lane; j < 128; j += 32) mx = fmaxf(mx, ss[r][j]);
-          for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-          const float me = mx == -INFINITY ? 0.f : mx;
-          float sum = 0.f;
-          for (int j = lane; j < 128; j += 32) {
-            const float p = ex2(ss[r][j] - me);
-            ss[r][j] = p;
-            sum += p;
-          }
-          for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-          __syncwarp();
-          if (lane == 0) {
-            const float al = ex2(mrow[r] - me);
-            arow[r] = al;
-            lrow[r] = lrow[r] * al + sum;
-            mrow[r] = mx;
-          }
-        }
-        __syncthreads();
-        if (tid < DV) {
-          for (int r = 0; r < kRowBlk; ++r) acc[r] *= arow[r];
-          for (int j = 0; j < nk; ++j) {
-            const float x = __bfloat162float(vb[static_cast<int64_t>(j) * a.HK * DV + tid]);
-            for (int r = 0; r < kRowBlk; ++r) acc[r] = fmaf(ss[r][j], x, acc[r]);
-          }
+        if (need) {
+          l_run *= alpha;
+          m_run = mx;
         }
       }
-      __syncthreads();
-      float* po = w.prefix ? a.po_p + slot * a.rows_p * DV : a.po_c + slot * a.rows_c * DV;
-      float2* ml = w.prefix ? a.ml_p + slot * a.rows_p : a.ml_c + slot * a.rows_c;
-      for (int r = 0; r < kRowBlk && r0 + r < rows; ++r) {
-        if (tid < DV) po[static_cast<int64_t>(r0 + r) * DV + tid] = acc[r];
-        if (tid == 0) ml[r0 + r] = make_float2(mrow[r], lrow[r]);
+      const float m_eff = m_run == -INFINITY ? 0.f : m_run;
+      float ps[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t pk[NC / 2];
+#pragma unroll
+      for (int e = 0; e < NC / 2; ++e) {
+        const float p0 = ex2(x[2 * e] - m_eff), p1 = ex2(x[2 * e + 1] - m_eff);
+        ps[e & 3] += p0 + p1;
+        pk[e] = pack_bf16x2(p0, p1);
+      }
+      l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+      if constexpr (NC >= 32) {
+#pragma unroll
+        for (int j = 0; j < NC / 32; ++j) tmem_st16(scol + (c0 >> 1) + 16 * j, pk + 16 * j);
+      } else {
+        // this warp writes the P chunks of its parity: its own, and zeros in the other quarters'
+        uint32_t z[NC / 2];
+#pragma unroll
+        for (int e = 0; e < NC / 2; ++e) z[e] = 0u;
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) {
+          const uint32_t at = scol + (2 * qq + hc) * (NC / 2);
+          const uint32_t* src = qq == quarter ? pk : z;
+          if constexpr (NC == 16) tmem_st8(at, src);
+          else tmem_st4(at, src);
+        }
+      }
+      return true;
+    };
+    for (int it = 0; it < n_iter; ++it) {
+      const bool rep = (w.prefix ? a.rep_p : a.rep_c) > 1;
+      const int rows = w.prefix ? a.rows_p : a.rows_c;
+      const bool active = (rep ? lane : r) < rows;
+      const bool done = rep ? tile(std::integral_constant<int, kN / 8>{}, true, it, active)
+                            : tile(std::integral_constant<int, kN / 2>{}, false, it, active);
+      if (!done) break;
+      const int lim = static_cast<int>(min64(kN, w.keys - w.tile * kN));
+      if (!w.prefix && lim < kN) {
+        // the V rows behind the sequence hold anything, and 0 x NaN is NaN: clear them
+        const int vs = it % C::kVStages, vu = it / C::kVStages;
+        if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBVF + vs), vu & 1, ctl, a.status,
+                                                    a.wait_limit_ns))))
+          break;
+        uint8_t* vt = smem + C::kVOff + vs * C::kVBytes;
+        const int n = (kN - lim) * (DV / 8);
+        for (int e = threadIdx.x - 64; e < n; e += 256) {
+          const int row = lim + e / (DV / 8), ch = e % (DV / 8);
+          *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kKPanel + row * 128 + (ch & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(BAR(kBPF + (it & 1)));
+      const Walk at = w;
+      first = it + 1 == n_iter || w.next(a);
+      if (first) {
+        // ------------------------------------------------------------ a part ends
+        if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), it & 1, ctl, a.status,
+                                                    a.wait_limit_ns))))
+          break;
+        tc_fence_after();
+        xch[hc * 128 + r] = l_run;
+        named_bar_sync(pair_bar, 64);
+        const float l = xch[r] + xch[128 + r];
+        const int64_t slot = at.seg + cta;
+        const int64_t row = rep ? (slot * 4 + quarter) * rows + lane : slot * rows + r;
+        float* po = (at.prefix ? a.po_p : a.po_c) + row * DV;
+#pragma unroll 1
+        for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
+          uint32_t ov[32];
+          tmem_ld32(tl + C::kOCol + c, ov);
+          tmem_wait_ld();
+          if (active) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(po + c + 4 * e) =
+                  make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          }
+        }
+        if (active && hc == 0) (at.prefix ? a.ml_p : a.ml_c)[row] = make_float2(m_run, l);
+        tc_fence_before();
+        m_run = -INFINITY;
+        l_run = 0.f;
       }
     }
-    u += n_tiles;
-    w.tile += n_tiles - 1;
-    if (u < f.u1) w.next(a);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // Abort path: no warp issues anything past the barrier above.  Wait (with a limit) for the
+  // copies and MMAs in flight before shared and tensor memory are released.
+  if (ctl->abort) {
+    if (lane == 0 && warp == 0) {
+      for (int q = max(0, issued_q - C::kQStages); q < issued_q; ++q)
+        mbar_wait_limited(BAR(kBQF + q % C::kQStages), (q / C::kQStages) & 1);
+      for (int it = max(0, issued_k - C::kKStages); it < issued_k; ++it)
+        mbar_wait_limited(BAR(kBKF + it % C::kKStages), (it / C::kKStages) & 1);
+    }
+    if (lane == 0 && warp == 10)
+      for (int it = max(0, issued_v - C::kVStages); it < issued_v; ++it)
+        mbar_wait_limited(BAR(kBVF + it % C::kVStages), (it / C::kVStages) & 1);
+    if (warp == 1) {
+      tc_fence_after();
+      if (elect_one()) {
+        umma_commit(BAR(kBDrain));
+        mbar_wait_limited(BAR(kBDrain), 0);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -261,8 +544,28 @@ __global__ void __launch_bounds__(256) cache_weights_kernel(const Args a) {
 
 template <int DQK, int DV>
 static int launch(const Args& a, cudaStream_t st) {
-  cache_part_kernel<DQK, DV><<<a.C, kSimple, 0, st>>>(a);
-  int rc = check_launch("cache attention kernel launch");
+  using C = Cfg<DQK, DV>;
+  static PerDeviceOnce attr;
+  int rc = once_per_device(attr, [] {
+    return cuda_error(cudaFuncSetAttribute(cache_part_kernel<DQK, DV>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem),
+                      "cache attention smem attribute");
+  });
+  if (rc) return rc;
+  Maps m;
+  if (!make_map(&m.qc, a.q, DQK, a.B, a.HQ, 1, 1, a.G) ||
+      !make_map(&m.kc, a.k, DQK, a.S, a.HK, a.B, C::kN) ||
+      !make_map(&m.vc, a.v, DV, a.S, a.HK, a.B, C::kN))
+    return SA_ERR_CUDA;
+  m.qp = m.qc;
+  m.kp = m.kc;
+  m.vp = m.vc;
+  if (a.P > 0 && (!make_map(&m.qp, a.q, DQK, a.B, a.HQ, 1, a.nb, a.G) ||
+                  !make_map(&m.kp, a.kp, DQK, a.P, a.HK, 1, C::kN) ||
+                  !make_map(&m.vp, a.vp, DV, a.P, a.HK, 1, C::kN)))
+    return SA_ERR_CUDA;
+  cache_part_kernel<DQK, DV><<<a.C, C::kThreads, C::kSmem, st>>>(m, a);
+  rc = check_launch("cache attention kernel launch");
   if (rc) return rc;
   cache_join_kernel<DV><<<static_cast<unsigned>(a.B * a.HQ), kJoin, 0, st>>>(a);
   rc = check_launch("cache join kernel launch");
@@ -283,15 +586,16 @@ static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
   a->Dv = p->Dv;
   a->S = p->S;
   a->P = p->P;
-  a->kn = 128;
+  a->kn = p->Dqk <= 128 ? 128 : 64;
   a->Sp = (p->S + 127) / 128 * 128;
   a->nb = 128 / a->G;
   if (a->nb > p->B) a->nb = p->B;
   a->Rt = (p->B + a->nb - 1) / a->nb;
   a->Tp = (p->P + a->kn - 1) / a->kn;
-  a->rep_p = a->rep_c = 1;
   a->rows_p = a->nb * a->G;
   a->rows_c = a->G;
+  a->rep_p = a->rows_p <= 32 ? 4 : 1;
+  a->rep_c = a->rows_c <= 32 ? 4 : 1;
   const size_t parts_p = p->P ? (static_cast<size_t>(a->HK) * a->Rt + kMaxCtas) * a->rep_p * a->rows_p : 0;
   const size_t parts_c = (static_cast<size_t>(p->B) * p->HK + kMaxCtas) * a->rep_c * a->rows_c;
   size_t off = 0;

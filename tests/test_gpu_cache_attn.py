@@ -218,3 +218,25 @@ def test_two_calls_at_once_on_two_streams():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("D", [D64, D128, D192, D256], ids=str)
+def test_short_wait_limit_reports_timeout_then_recovers(D):
+    """A wait limit below 1 us makes ordinary waits run out: the call returns, reports it and
+    leaves the context usable."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    c = Case([700, 1, 333], HQ=8, HK=2, D=D, P=400, seed=51)
+    want = sa.cache_attn_fwd(**c.g, with_weights=True)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    try:
+        sa.sparse_attn_set_wait_limit_ns(300)
+        sa.cache_attn_fwd(**c.g, with_weights=True, dev_status=status)
+        torch.cuda.synchronize()
+    finally:
+        sa.sparse_attn_set_wait_limit_ns(0)
+    assert int(status.item()) & _lib.SA_STATUS_TIMEOUT
+    status.zero_()
+    got = sa.cache_attn_fwd(**c.g, with_weights=True, dev_status=status)
+    assert int(status.item()) == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
