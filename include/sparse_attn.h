@@ -432,7 +432,7 @@ typedef struct cache_evict_params {
  *   weights_out      the kept keys' weights, then zeros up to S_out (what tokens appended
  *                    later start from);
  *   lens_out[b]      min(lens[b], budget).
- * The outputs must not overlap the inputs (SA_ERR_INVALID for equal base pointers).
+ * No output may overlap an input or another output (SA_ERR_INVALID).
  * 1 <= budget <= S_out, sinks, recent >= 0, sinks + recent <= budget.  A length outside
  * [0, S] is clamped and sets SA_STATUS_INDEX in *dev_status.  Needs no workspace.
  */

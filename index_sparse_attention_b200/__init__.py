@@ -24,7 +24,8 @@ __all__ = ["BlockSparse", "block_mask_to_block_sparse", "index_to_block_sparse",
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _on_device(arg):
@@ -40,6 +41,8 @@ def _on_device(arg):
         def wrapper(*args, **kw):
             t = kw.get(arg) if arg in kw else (args[pos] if pos < len(args) else None)
             if isinstance(t, torch.Tensor) and t.is_cuda:
+                if type(t) is torch.Tensor and t.get_device() == torch.cuda.current_device():
+                    return fn(*args, **kw)
                 with torch.cuda.device(t.device):
                     return fn(*args, **kw)
             return fn(*args, **kw)
@@ -61,6 +64,13 @@ def _require(cond, msg, exc=ValueError):
 def _check(name, t, dtype, shape=None, ndim=None, device=None, contiguous=True):
     """Argument checks done here because the C ABI sees pointers and sizes only: a
     tensor of the wrong shape would be read or written out of bounds by the kernels."""
+    # a tensor that passes is let through before any message is put together: the messages
+    # take longer than the checks (a call of ten tensors: 60 us of host time against 10)
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda
+            and (shape is None or t.shape == shape) and (ndim is None or t.dim() == ndim)
+            and (not contiguous or t.is_contiguous())
+            and (device is None or t.device == device)):
+        return
     _require(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor", TypeError)
     _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}", TypeError)
     if ndim is not None:
@@ -489,13 +499,16 @@ def cache_evict(k_cache, v_cache, weights, lens, budget, sinks=0, recent=0, k_ou
     if keep is None:
         keep = torch.empty((B, HK, budget), dtype=torch.int32, device=dev)
     _check("keep", keep, torch.int32, shape=(B, HK, budget), device=dev)
-    _require_apart((k_cache, v_cache, weights, lens), (k_out, v_out, weights_out, lens_out, keep))
     p = _lib.CacheEvictStruct(
         k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), lens.data_ptr(),
         k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(), lens_out.data_ptr(),
         keep.data_ptr(), B, HK, Dqk, Dv, S, S_out, budget, sinks, recent,
         None if dev_status is None else dev_status.data_ptr())
-    _lib.check("cache_evict", L.cache_evict(ctypes.byref(p), _stream(dev)))
+    code = L.cache_evict(ctypes.byref(p), _stream(dev))
+    if code == _lib.SA_ERR_INVALID:  # (every other cause has been checked above)
+        _require_apart((k_cache, v_cache, weights, lens),
+                       (k_out, v_out, weights_out, lens_out, keep))
+    _lib.check("cache_evict", code)
     return k_out, v_out, weights_out, lens_out, keep
 
 

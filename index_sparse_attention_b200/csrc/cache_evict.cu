@@ -179,15 +179,29 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
     return SA_ERR_INVALID;
   if (static_cast<int64_t>(p->sinks) + p->recent > p->budget || p->budget > p->S_out)
     return SA_ERR_INVALID;
-  if (p->k_out == p->k_cache || p->v_out == p->v_cache || p->weights_out == p->weights ||
-      p->lens_out == p->lens)
-    return SA_ERR_INVALID;
   const bool dims = (p->Dqk == 64 && p->Dv == 64) || (p->Dqk == 128 && p->Dv == 128) ||
                     (p->Dqk == 192 && p->Dv == 128) || (p->Dqk == 256 && p->Dv == 256);
   if (!dims) return SA_ERR_UNSUPPORTED;
   if (p->B > 65535 || p->S > 0x7FFFFF00 || p->S_out > 0x7FFFFF00 || p->HK > 65535 ||
       static_cast<int64_t>(p->B) * p->HK > 0x7FFFFFFF)
     return SA_ERR_UNSUPPORTED;
+  // no output may share memory with an input or another output
+  const int64_t BH = static_cast<int64_t>(p->B) * p->HK;
+  if (p->S > (int64_t(1) << 40) / BH || p->S_out > (int64_t(1) << 40) / BH)
+    return SA_ERR_UNSUPPORTED;  // (beyond any memory; keeps the products below in range)
+  struct Span {
+    const void* at;
+    int64_t bytes;
+  } const spans[] = {{p->k_cache, BH * p->S * p->Dqk * 2}, {p->v_cache, BH * p->S * p->Dv * 2},
+                     {p->weights, BH * p->S * 4},          {p->lens, p->B * 4ll},
+                     {p->k_out, BH * p->S_out * p->Dqk * 2}, {p->v_out, BH * p->S_out * p->Dv * 2},
+                     {p->weights_out, BH * p->S_out * 4},  {p->lens_out, p->B * 4ll},
+                     {p->keep, BH * p->budget * 4}};
+  for (int i = 4; i < 9; ++i)
+    for (int j = 0; j < i; ++j) {
+      const char *x = static_cast<const char*>(spans[i].at), *y = static_cast<const char*>(spans[j].at);
+      if (x < y + spans[j].bytes && y < x + spans[i].bytes) return SA_ERR_INVALID;
+    }
   const void* ptrs[] = {p->k_cache, p->v_cache, p->k_out, p->v_out};
   for (const void* x : ptrs)
     if ((reinterpret_cast<uintptr_t>(x) & 15u) != 0) return SA_ERR_ALIGN;

@@ -100,7 +100,8 @@ def test_key_weights_refusals(lib):
     (dict(k_cache=None), BAD), (dict(weights=None), BAD), (dict(lens=None), BAD),
     (dict(k_out=None), BAD), (dict(keep=None), BAD), (dict(lens_out=None), BAD),
     (dict(k_out=0x100000), BAD), (dict(v_out=0x200000), BAD), (dict(weights_out=0x300000), BAD),
-    (dict(lens_out=0x400000), BAD), (dict(Dqk=80), UNSUP), (dict(B=65536), UNSUP),
+    (dict(lens_out=0x400000), BAD), (dict(k_out=0x100000 + 102384), BAD),
+    (dict(v_out=0x500000 - 102384), BAD), (dict(keep=0x700010), BAD), (dict(Dqk=80), UNSUP), (dict(B=65536), UNSUP),
     (dict(S=1 << 40), UNSUP), (dict(k_cache=0x100008), _lib.SA_ERR_ALIGN),
 ], ids=str)
 def test_eviction_refusals(lib, kw, code):
@@ -170,7 +171,6 @@ def test_binding_refuses_wrong_shapes(lib, cuda_check_off):
         ("k_out must have shape", (k, v, w, lens, 4), dict(k_out=bf(2, 8, 2, 64))),
         ("v_out must have shape", (k, v, w, lens, 4), dict(k_out=bf(2, 8, 2, 128), v_out=bf(2, 9, 2, 128))),
         ("keep must have shape", (k, v, w, lens, 4), dict(keep=torch.zeros(2, 2, 5, dtype=torch.int32))),
-        ("overlaps", (k, v, w, lens, 4), dict(k_out=k)),
     ]:
         with pytest.raises((ValueError, TypeError), match=match):
             sa.cache_evict(*args, **kw)
