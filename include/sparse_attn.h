@@ -399,7 +399,7 @@ size_t cache_attn_workspace_size(const cache_attn_params *p);
  * not read (Dv still selects the head-dim pair).  A query whose lse is -inf adds nothing.
  *   weights, weights_out  fp32 [B][HK][Sk]; may be the same array.
  * The sums are taken in a fixed order (two calls give identical bits).  `workspace`: device
- * memory of at least sparse_attn_key_weights_workspace_size() bytes (which may be 0),
+ * memory of at least sparse_attn_key_weights_workspace_size() bytes,
  * 16-byte aligned, not initialised.
  */
 int sparse_attn_key_weights(const sparse_attn_params *p, const float *weights,

@@ -7,58 +7,154 @@
 // queries is a sum along the columns one thread holds: no exchange between lanes, no atomics,
 // one store per key, and a fixed order.
 //
-// B200 design: a CTA owns 128 keys of one (batch, KV head), its K tile stays in shared memory
-// and the query tiles of the key-to-query list stream past it, for every query head of the
-// group:
-//   warp 0     TMA: K once, then Q tiles of kBN queries, kStages deep;
-//   warp 1     tcgen05.mma S^T = K Q^T (128 keys x kBN queries) into one of two TMEM buffers;
-//   warps 2-5  thread = key row: exp2(S^T scale log2e - lse log2e) summed over the columns.
-//              A step's lse values (one query per thread, fetched a step ahead) pass through
-//              shared memory; the presence words of index mode are fetched a step ahead too and
-//              transposed across the warp.  Steps are summed on their own before they join the
-//              running sum, so that long query ranges do not lose low bits.
-// Two CTAs share an SM at head dims up to 192, so that one's prologue and waits overlap the
-// other's work.  With fewer key tiles than SMs can hold, the query range is split and the
-// parts are added by a second kernel.  Every mbarrier wait is bounded (sa_device.cuh).
+// B200 design: one persistent CTA per SM.  The work is a row of units, one 128 x 128 tile of
+// one query head each: key tile after key tile (an item: 128 keys of one (batch, KV head)),
+// inside it the query tiles of its list, inside them the heads of the group (which share the
+// tile's masks).  CTA c of C takes units [U c / C, U (c + 1) / C), so that ragged lists and
+// causal triangles load the SMs evenly.  An item inside one CTA is stored at once; the two ends
+// of a CTA's range can be cut items, whose parts go to the workspace and are added by a second
+// kernel in CTA order.
+//   warp 0     TMA: an item's K tile and the Q tiles, several stages deep;
+//   warp 1     tcgen05.mma S^T = K Q^T into one of four TMEM buffers;
+//   warps 2-9  two warpgroups that take the units in turn (thread = key row):
+//              exp2(S^T scale log2e - lse log2e) summed over the 128 queries.  A unit's lse
+//              values (one per thread, fetched a unit ahead) pass through shared memory; the
+//              presence words of index mode are transposed across the warp.  Each unit is summed
+//              on its own before it joins the running sum, so that long query ranges do not lose
+//              low bits.
+// Every mbarrier wait is bounded (sa_device.cuh).
 #include "sa_device.cuh"
 #include "sa_kernels.h"
 
 namespace sa {
 namespace kweights {
 
+constexpr int kThreads = 320;
+constexpr int kMaxCtas = 256;
+
 template <int DQK>
 struct Cfg {
-  static constexpr int kBN = DQK <= 128 ? 128 : 64;  // queries per step
-  static constexpr int kStages = DQK == 64 ? 4 : DQK == 256 ? 4 : 2;
-  static constexpr int kCtas = DQK == 256 ? 1 : 2;   // per SM
-  static constexpr int kKPanel = 128 * 128;
-  static constexpr int kQPanel = kBN * 128;
-  static constexpr int kKBytes = 128 * DQK * 2;
-  static constexpr int kQBytes = kBN * DQK * 2;
-  static constexpr int kQOff = kKBytes;
-  static constexpr int kLOff = kQOff + kStages * kQBytes;  // lse of a step, [2][kBN]
-  static constexpr int kBarOff = kLOff + 2 * kBN * 4;
-  static constexpr int kSmem = kBarOff + 128 + 1024;
-  static constexpr uint32_t kTmemCols = 2 * kBN;
-  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory budget");
+  static constexpr int kKStages = DQK <= 128 ? 2 : 1;
+  static constexpr int kQStages = DQK == 64 ? 6 : DQK == 128 ? 4 : DQK == 192 ? 3 : 2;
+  static constexpr int kPanel = 128 * 128;  // 64 columns x 128 rows
+  static constexpr int kTile = 128 * DQK * 2;
+  static constexpr int kQOff = kKStages * kTile;
+  static constexpr int kLOff = kQOff + kQStages * kTile;  // lse [2 warpgroups][2][128]
+  static constexpr int kXOff = kLOff + 2 * 2 * 128 * 4;   // part sums of warpgroup 1, [2][128]
+  static constexpr int kFindOff = kXOff + 2 * 128 * 4;
+  static constexpr int kBarOff = kFindOff + 80 * 4;
+  static constexpr int kSmem = kBarOff + 256 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
-enum : int { kBK = 0, kBQF = 1, kBQE = 5, kBSF = 9, kBSE = 11, kBDrain = 13, kNumBars = 14 };
+enum : int { kBKF = 0, kBKE = 2, kBQF = 4, kBQE = 10, kBSF = 16, kBSE = 20, kBDrain = 24,
+             kNumBars = 25 };
 
 struct Args {
   AttnArgs t;
   const float* w_in;
   float* w_out;
-  float* part;  // [splits][B * HK][Sk] when splits > 1
-  int splits;
+  // workspace: the parts of cut items -- an item that begins in CTA c and goes on: tail[c],
+  // then head[c + 1 ..]; fix[c]: that item (or -1) and the last CTA that holds a part of it
+  float *head, *tail;  // [kMaxCtas][128]
+  int2* fix;           // [kMaxCtas]
+  int items, C, G;
 };
 
+// Place of a unit: item (key tile of a KV head), list entry, head of the group.
+struct Cursor {
+  int item, n, n_full;  // list entries of the item (> 0), the full ones
+  int k, hh;
+  int tile, tile_next;  // list entries k and k + 1
+  const int32_t* list;
+  __device__ __forceinline__ void open(const Args& a, int it, int kk) {
+    item = it;
+    n_full = __ldg(a.t.tcnt + 2 * static_cast<int64_t>(it));
+    n = n_full + __ldg(a.t.tcnt + 2 * static_cast<int64_t>(it) + 1);
+    list = a.t.tidx + static_cast<int64_t>(it) * a.t.Tm;
+    k = kk;
+    if (kk < n) {
+      tile = __ldg(list + kk);
+      tile_next = kk + 1 < n ? __ldg(list + kk + 1) : 0;
+    }
+  }
+  // to the next unit; false past the last item
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (++hh < a.G) return true;
+    hh = 0;
+    if (++k < n) {
+      tile = tile_next;
+      tile_next = k + 1 < n ? __ldg(list + k + 1) : 0;
+      return true;
+    }
+    for (int i = item + 1; i < a.items; ++i) {
+      open(a, i, 0);
+      if (n > 0) return true;
+    }
+    return false;
+  }
+};
+
+// This CTA's units, the item the first one lies in and the units before that item; called by
+// the whole block, ends with a barrier.
+struct Found {
+  int64_t U, u0, u1, off;
+  int item, C;
+};
+__device__ __forceinline__ Found find_range(const Args& a, int c, int* sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.items + kThreads - 1) / kThreads;
+  const int i0 = min(tid * per, a.items), i1 = min(i0 + per, a.items);
+  auto entries = [&](int i) {
+    return __ldg(a.t.tcnt + 2 * static_cast<int64_t>(i)) +
+           __ldg(a.t.tcnt + 2 * static_cast<int64_t>(i) + 1);
+  };
+  int mine = 0;
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) mine += entries(i);
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += t;
+  }
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int t = sh[w];
+    if (w < warp) before += t;
+    total += t;
+  }
+  Found f;
+  f.U = static_cast<int64_t>(total) * a.G;
+  f.C = static_cast<int>(min64(a.C, f.U));
+  f.u0 = c < f.C ? f.U * c / f.C : f.U;
+  f.u1 = c < f.C ? f.U * (c + 1) / f.C : f.U;
+  const int target = static_cast<int>(f.u0 / a.G);  // the entry that the first unit lies in
+  int at = before + incl - mine;
+  if (target >= at && target < at + mine) {
+    for (int i = i0; i < i1; ++i) {
+      const int t = entries(i);
+      if (target < at + t) {
+        sh[64] = i;
+        sh[65] = at;
+        break;
+      }
+      at += t;
+    }
+  }
+  __syncthreads();
+  f.item = f.u0 < f.u1 ? sh[64] : 0;
+  f.off = f.u0 < f.u1 ? static_cast<int64_t>(sh[65]) * a.G : 0;
+  return f;
+}
+
 template <int DQK>
-__global__ void __launch_bounds__(192, Cfg<DQK>::kCtas)
+__global__ void __launch_bounds__(kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const Args ka) {
   using C = Cfg<DQK>;
-  constexpr int BN = C::kBN;
   const AttnArgs& a = ka.t;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -68,247 +164,274 @@ __global__ void __launch_bounds__(192, Cfg<DQK>::kCtas)
   volatile WaitCtl* ctl =
       reinterpret_cast<volatile WaitCtl*>(smem + C::kBarOff + 8 * kNumBars + 4);
   auto BAR = [&](int k) { return sbase + C::kBarOff + 8u * static_cast<uint32_t>(k); };
-
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the key tiles with the longest lists under causal (the first ones) start first
-  const int bgs = a.B * a.HK;
-  int lin = static_cast<int>(blockIdx.x);
-  const int nt = lin / (bgs * ka.splits);
-  lin -= nt * bgs * ka.splits;
-  const int sp = lin / bgs, bgi = lin - sp * bgs;
-  const int b = bgi / a.HK, g = bgi - b * a.HK;
-  const int G = a.HQ / a.HK;
-  const int64_t bg = bgi;
-  const int64_t trow = bg * a.Tn + nt;
-  const int n_full = __ldg(a.tcnt + 2 * trow);
-  const int n_mt = n_full + __ldg(a.tcnt + 2 * trow + 1);
-  const int32_t* tlist = a.tidx + trow * a.Tm;
-  constexpr int kSub = 128 / BN;
-  const int64_t n_all = static_cast<int64_t>(G) * n_mt * kSub;  // (head, query tile, part)
-  const int64_t it0 = n_all * sp / ka.splits;
-  const int n_iter = static_cast<int>(n_all * (sp + 1) / ka.splits - it0);
-  int issued = 0;
+  const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    mbar_init(BAR(kBK), 1);
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(BAR(kBQF + s), 1);
-      mbar_init(BAR(kBQE + s), 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(BAR(kBSF + s), 1);
-      mbar_init(BAR(kBSE + s), 128);
-    }
-    mbar_init(BAR(kBDrain), 1);
+    for (int k = 0; k < kNumBars; ++k) mbar_init(BAR(k), k >= kBSE && k < kBSE + 4 ? 128 : 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const Found f = find_range(ka, cta, reinterpret_cast<int*>(smem + C::kFindOff));
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-
-  // step -> query head, first query, whether the tile is partial
-  auto decode = [&](int it, int& h, int& m0, bool& partial) {
-    const int64_t x = it0 + it;
-    const int per_head = n_mt * kSub;
-    const int hh = static_cast<int>(x / per_head);
-    const int rest = static_cast<int>(x - static_cast<int64_t>(hh) * per_head);
-    const int k = rest / kSub;
-    h = g * G + hh;
-    m0 = __ldg(tlist + k) * 128 + (rest % kSub) * BN;
-    partial = k >= n_full;
-  };
+  const int n_iter = static_cast<int>(f.u1 - f.u0);
+  if (n_iter == 0 && threadIdx.x == 0) ka.fix[cta] = make_int2(-1, 0);
+  Cursor cur{};
+  if (n_iter > 0) {
+    const int64_t r = f.u0 - f.off;
+    cur.open(ka, f.item, static_cast<int>(r / ka.G));
+    cur.hh = static_cast<int>(r - static_cast<int64_t>(cur.k) * ka.G);
+  }
+  int issued_q = 0, issued_k = 0;
 
   if (warp == 0) {
-    if (n_iter > 0) {
+    // ---------------------------------------------------------------- producer
+    int item = -1;
+    for (int it = 0; it < n_iter; ++it) {
+      const int bg = cur.item / a.Tn, b = bg / a.HK, g = bg - b * a.HK;
+      if (cur.item != item) {
+        item = cur.item;
+        const int ks = issued_k % C::kKStages, ku = issued_k / C::kKStages;
+        if (!warp_wait(BAR(kBKE + ks), (ku & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(BAR(kBKF + ks), C::kTile);
+          for (int c = 0; c < DQK / 64; ++c)
+            tma_load_4d(sbase + ks * C::kTile + c * C::kPanel, &tm_k, BAR(kBKF + ks), c * 64,
+                        (item - bg * a.Tn) * 128, g, b);
+        }
+        __syncwarp();
+        ++issued_k;
+      }
+      const int st = it % C::kQStages, u = it / C::kQStages;
+      if (!warp_wait(BAR(kBQE + st), (u & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
+      const int m0 = __shfl_sync(0xFFFFFFFFu, cur.tile, 0) * 128;
       if (elect_one()) {
-        prefetch_tensormap(&tm_q);
-        mbar_arrive_expect_tx(BAR(kBK), C::kKBytes);
+        mbar_arrive_expect_tx(BAR(kBQF + st), C::kTile);
         for (int c = 0; c < DQK / 64; ++c)
-          tma_load_4d(sbase + c * C::kKPanel, &tm_k, BAR(kBK), c * 64, nt * 128, g, b);
+          tma_load_4d(sbase + C::kQOff + st * C::kTile + c * C::kPanel, &tm_q, BAR(kBQF + st),
+                      c * 64, m0, g * ka.G + cur.hh, b);
       }
       __syncwarp();
-      for (int it = 0; it < n_iter; ++it) {
-        int h, m0;
-        bool partial;
-        decode(it, h, m0, partial);
-        m0 = __shfl_sync(0xFFFFFFFFu, m0, 0);
-        const int st = it % C::kStages, u = it / C::kStages;
-        if (!warp_wait(BAR(kBQE + st), (u & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(BAR(kBQF + st), C::kQBytes);
-          for (int c = 0; c < DQK / 64; ++c)
-            tma_load_4d(sbase + C::kQOff + st * C::kQBytes + c * C::kQPanel, &tm_q, BAR(kBQF + st),
-                        c * 64, m0, h, b);
-        }
-        __syncwarp();
-        issued = it + 1;
-      }
-      // the last arrivals on the stages' barriers have landed before the CTA may leave
-      if (issued == n_iter)
-        for (int it = max(0, n_iter - C::kStages); it < n_iter; ++it)
-          if (!warp_wait(BAR(kBQE + it % C::kStages), (it / C::kStages) & 1, ctl, a.status,
-                         a.wait_limit_ns))
-            break;
+      issued_q = it + 1;
+      if (it + 1 < n_iter) cur.next(ka);
+    }
+    // the last arrivals on the stages' barriers have landed before the CTA may leave
+    if (issued_q == n_iter) {
+      for (int it = max(0, n_iter - C::kQStages); it < n_iter; ++it)
+        if (!warp_wait(BAR(kBQE + it % C::kQStages), (it / C::kQStages) & 1, ctl, a.status,
+                       a.wait_limit_ns))
+          break;
+      for (int k = max(0, issued_k - C::kKStages); k < issued_k; ++k)
+        if (!warp_wait(BAR(kBKE + k % C::kKStages), (k / C::kKStages) & 1, ctl, a.status,
+                       a.wait_limit_ns))
+          break;
     }
   } else if (warp == 1) {
-    if (n_iter > 0) {
-      constexpr uint32_t idesc = idesc_bf16(128, BN, 0, 0);
-      const uint64_t kd = sw128_desc(sbase, 16, 1024);
-      bool ok = warp_wait(BAR(kBK), 0, ctl, a.status, a.wait_limit_ns);
-      for (int it = 0; ok && it < n_iter; ++it) {
-        const int st = it % C::kStages, u = it / C::kStages, sb = it & 1;
-        if (!warp_wait(BAR(kBQF + st), u & 1, ctl, a.status, a.wait_limit_ns)) break;
-        if (!warp_wait(BAR(kBSE + sb), ((it >> 1) & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
-        tc_fence_after();
-        const uint64_t qd = sw128_desc(sbase + C::kQOff + st * C::kQBytes, 16, 1024);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < DQK / 16; ++kk)
-            umma_ss(tmem + sb * BN, kd + (((kk >> 2) * C::kKPanel + (kk & 3) * 32) >> 4),
-                    qd + (((kk >> 2) * C::kQPanel + (kk & 3) * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
-          umma_commit(BAR(kBSF + sb));
-          umma_commit(BAR(kBQE + st));
-        }
-        __syncwarp();
+    // ---------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = idesc_bf16(128, 128, 0, 0);
+    int item = -1, part = -1;
+    for (int it = 0; it < n_iter; ++it) {
+      if (cur.item != item) {
+        item = cur.item;
+        ++part;
+        if (!warp_wait(BAR(kBKF + part % C::kKStages), (part / C::kKStages) & 1, ctl, a.status,
+                       a.wait_limit_ns))
+          break;
       }
+      const int st = it % C::kQStages, u = it / C::kQStages, sb = it & 3;
+      if (!warp_wait(BAR(kBQF + st), u & 1, ctl, a.status, a.wait_limit_ns)) break;
+      if (!warp_wait(BAR(kBSE + sb), ((it >> 2) & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
+      tc_fence_after();
+      const bool more = it + 1 < n_iter;
+      if (more) cur.next(ka);
+      const int ks = part % C::kKStages;
+      const uint64_t kd = sw128_desc(sbase + ks * C::kTile, 16, 1024);
+      const uint64_t qd = sw128_desc(sbase + C::kQOff + st * C::kTile, 16, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < DQK / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
+          umma_ss(tmem + sb * 128, kd + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(BAR(kBSF + sb));
+        umma_commit(BAR(kBQE + st));
+        if (!more || cur.item != item) umma_commit(BAR(kBKE + ks));
+      }
+      __syncwarp();
     }
   } else {
-    const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;
-    const int64_t j = static_cast<int64_t>(nt) * 128 + r;
-    const bool key_ok = j < a.Sk;
+    // ---------------------------------------------------------------- exponentials and sums
+    const int quarter = warp & 3, wg = (warp - 2) >> 2;
+    const int r = quarter * 32 + lane;       // key row of the item = TMEM lane
+    const int tq = (threadIdx.x - 64) & 127;  // the query of a unit whose lse this thread fetches
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    float* lbuf = reinterpret_cast<float*>(smem + C::kLOff);
-    const int tq = threadIdx.x - 64;  // the query of a step whose lse this thread fetches
-    constexpr int kWords = BN / 32;
+    float* lbuf = reinterpret_cast<float*>(smem + C::kLOff) + wg * 256;
+    float* xch = reinterpret_cast<float*>(smem + C::kXOff);
+    const float sc = a.scale_log2;
+    // `nxt` runs one of this warpgroup's units ahead of `cur` and fetches its lse
     float l_nxt = 0.f;
-    uint32_t w_nxt[kWords];
-    auto fetch = [&](int it) {
-      if (it >= n_iter) return;
-      int h, m0;
-      bool partial;
-      decode(it, h, m0, partial);
-      if (tq < BN) {
-        const int64_t i = static_cast<int64_t>(m0) + tq;
-        // (a row past Sq, or one that saw no key, adds nothing: exp2(-inf))
-        float l = -INFINITY;
-        if (i < a.Sq) l = __ldg(a.lse + (static_cast<int64_t>(b) * a.HQ + h) * a.Sq + i);
-        l_nxt = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-      }
-      if (partial && a.mode == SA_MODE_INDEX) {
-        // presence word of query m0 + 32 c + lane over this warp's 32 keys
-#pragma unroll
-        for (int c = 0; c < kWords; ++c) {
-          const int64_t i = static_cast<int64_t>(m0) + 32 * c + lane;
-          const int w = nt * 4 + quarter;
-          w_nxt[c] = (i < a.Sq && w < a.W) ? __ldg(a.bitmap + (bg * a.Sq + i) * a.W + w) : 0u;
-        }
+    Cursor nxt = cur;
+    bool more = n_iter > 0;   // nxt is a unit of this CTA
+    int it_n = 0;             // and its number
+    auto fetch = [&]() {
+      if (!more) return;
+      const int bg = nxt.item / a.Tn, b = bg / a.HK, g = bg - b * a.HK;
+      const int64_t i = static_cast<int64_t>(nxt.tile) * 128 + tq;
+      // (a row past Sq, or one that saw no key, adds nothing: exp2(-inf))
+      float l = -INFINITY;
+      if (i < a.Sq)
+        l = __ldg(a.lse + (static_cast<int64_t>(b) * a.HQ + g * ka.G + nxt.hh) * a.Sq + i);
+      l_nxt = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+    };
+    auto advance = [&](int by) {
+      for (int x = 0; x < by && more; ++x) {
+        ++it_n;
+        more = it_n < n_iter && nxt.next(ka);
       }
     };
-    fetch(0);
-    float total = 0.f;
+    advance(wg);
+    fetch();
+    uint32_t cm[4] = {0u, 0u, 0u, 0u};  // which of the tile's queries see this key
+    int cm_item = -1, cm_k = -1;
     bool ok = true;
-    for (int it = 0; it < n_iter; ++it) {
-      int h, m0;
-      bool partial;
-      decode(it, h, m0, partial);
-      const int sb = it & 1;
-      float* ls = lbuf + sb * BN;
-      if (tq < BN) ls[tq] = l_nxt;
-      uint32_t cm[kWords];
+    int part = 0;
+    int it = 0;
+    int64_t start = f.off;  // first unit of the item
+    bool cut_here = false;
+    while (it < n_iter) {
+      // ------------------------------------------------------------ one part: units of an item
+      const int item = cur.item;
+      const int64_t end = start + static_cast<int64_t>(cur.n) * ka.G;
+      const int it_end = static_cast<int>(min64(end, f.u1) - f.u0);
+      const int bg = item / a.Tn, nt = item - bg * a.Tn;
+      const int64_t j = static_cast<int64_t>(nt) * 128 + r;
+      const bool key_ok = j < a.Sk;
+      float total = 0.f;
+      for (; it < it_end; ++it) {
+        if ((it & 1) == wg) {
+          const int sb = it & 3;
+          float* ls = lbuf + ((it >> 1) & 1) * 128;
+          ls[tq] = l_nxt;
+          advance(2);
+          fetch();
+          const bool partial = cur.k >= cur.n_full;
+          if (partial && (cm_k != cur.k || cm_item != item)) {
+            cm_k = cur.k;
+            cm_item = item;
 #pragma unroll
-      for (int c = 0; c < kWords; ++c) cm[c] = 0xFFFFFFFFu;
-      if (partial) {
-#pragma unroll
-        for (int c = 0; c < kWords; ++c) {
-          const int64_t q0 = static_cast<int64_t>(m0) + 32 * c;
-          uint32_t x = key_ok ? 0xFFFFFFFFu : 0u;
-          if (a.causal) {  // i >= j
-            const int64_t lo = j - q0;
-            x &= lo <= 0 ? 0xFFFFFFFFu : (lo >= 32 ? 0u : (0xFFFFFFFFu << lo));
-          }
-          if (a.mode == SA_MODE_BLOCK && a.bs == 64 && key_ok) {
-            const int64_t mb = q0 / 64;
-            const bool m = mb < a.Mb &&
-                           __ldg(a.mask + (bg * a.Mb + mb) * static_cast<int64_t>(a.Nb) + j / 64) != 0;
-            if (!m) x = 0u;
-          } else if (a.mode == SA_MODE_INDEX) {
-            x &= warp_transpose32(w_nxt[c], lane);
-          }
-          cm[c] = x;
-        }
-      }
-      fetch(it + 1);
-      // (the four warps meet once a step: the other lse buffer is free, this one is full;
-      // they also leave together)
-      const bool w_ok = __all_sync(
-          0xFFFFFFFFu, mbar_wait(BAR(kBSF + sb), (it >> 1) & 1, ctl, a.status, a.wait_limit_ns));
-      if (!named_bar_and(1, 128, w_ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const float4* ls4 = reinterpret_cast<const float4*>(ls);
-      const float sc = a.scale_log2;
-      float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < kWords; ++c) {
-        uint32_t s[32];
-        tmem_ld32(tl + sb * BN + 32 * c, s);
-        tmem_wait_ld();
-        if (c == kWords - 1) {  // every column is read: the buffer is free
-          tc_fence_before();
-          mbar_arrive(BAR(kBSE + sb));
-        }
-        if (!partial) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 l = ls4[8 * c + e];
-            ps[0] += ex2(fmaf(__uint_as_float(s[4 * e]), sc, -l.x));
-            ps[1] += ex2(fmaf(__uint_as_float(s[4 * e + 1]), sc, -l.y));
-            ps[2] += ex2(fmaf(__uint_as_float(s[4 * e + 2]), sc, -l.z));
-            ps[3] += ex2(fmaf(__uint_as_float(s[4 * e + 3]), sc, -l.w));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 l = ls4[8 * c + e];
-            const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const float p = ex2(fmaf(__uint_as_float(s[4 * e + t]), sc, -lv[t]));
-              ps[t] += ((cm[c] >> (4 * e + t)) & 1u) ? p : 0.f;
+            for (int c = 0; c < 4; ++c) {
+              const int64_t q0 = static_cast<int64_t>(cur.tile) * 128 + 32 * c;
+              uint32_t x = key_ok ? 0xFFFFFFFFu : 0u;
+              if (a.causal) {  // i >= j
+                const int64_t lo = j - q0;
+                x &= lo <= 0 ? 0xFFFFFFFFu : (lo >= 32 ? 0u : (0xFFFFFFFFu << lo));
+              }
+              if (a.mode == SA_MODE_BLOCK && a.bs == 64 && key_ok) {
+                const int64_t mb = q0 / 64;
+                if (!(mb < a.Mb &&
+                      __ldg(a.mask + (static_cast<int64_t>(bg) * a.Mb + mb) * a.Nb + j / 64) != 0))
+                  x = 0u;
+              } else if (a.mode == SA_MODE_INDEX) {
+                // lane L loads the presence word of query q0 + L over this warp's 32 keys; the
+                // transpose leaves in lane L the word of key L over the 32 queries
+                const int64_t i = q0 + lane;
+                const int w = nt * 4 + quarter;
+                const uint32_t bits =
+                    (i < a.Sq && w < a.W)
+                        ? __ldg(a.bitmap + (static_cast<int64_t>(bg) * a.Sq + i) * a.W + w)
+                        : 0u;
+                x &= warp_transpose32(bits, lane);
+              }
+              cm[c] = x;
             }
           }
+          if (ok)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBSF + sb), (it >> 2) & 1, ctl, a.status,
+                                                   a.wait_limit_ns));
+          named_bar_sync(1 + wg, 128);  // the unit's lse values are in shared memory
+          if (ok) {
+            tc_fence_after();
+            const float4* ls4 = reinterpret_cast<const float4*>(ls);
+            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_ld32(tl + sb * 128 + 32 * c, s);
+              tmem_wait_ld();
+              if (c == 3) {  // every column is read: the buffer is free
+                tc_fence_before();
+                mbar_arrive(BAR(kBSE + sb));
+              }
+              if (!partial) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 l = ls4[8 * c + e];
+                  ps[0] += ex2(fmaf(__uint_as_float(s[4 * e]), sc, -l.x));
+                  ps[1] += ex2(fmaf(__uint_as_float(s[4 * e + 1]), sc, -l.y));
+                  ps[2] += ex2(fmaf(__uint_as_float(s[4 * e + 2]), sc, -l.z));
+                  ps[3] += ex2(fmaf(__uint_as_float(s[4 * e + 3]), sc, -l.w));
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 l = ls4[8 * c + e];
+                  const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                  for (int t = 0; t < 4; ++t) {
+                    const float p = ex2(fmaf(__uint_as_float(s[4 * e + t]), sc, -lv[t]));
+                    ps[t] += ((cm[c] >> (4 * e + t)) & 1u) ? p : 0.f;
+                  }
+                }
+              }
+            }
+            total += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+          }
+        }
+        if (it + 1 < n_iter) cur.next(ka);
+      }
+      // ------------------------------------------------------------ the part's sum
+      float* xp = xch + (part & 1) * 128;
+      if (wg == 1) xp[r] = total;
+      named_bar_sync(3, 256);
+      if (wg == 0) {
+        total += xp[r];
+        const bool begins = start >= f.u0, ends = end <= f.u1;
+        if (begins && ends) {
+          if (key_ok) {
+            const int64_t at = static_cast<int64_t>(bg) * a.Sk + j;
+            ka.w_out[at] = ka.w_in ? ka.w_in[at] + total : total;
+          }
+        } else if (begins) {
+          ka.tail[cta * 128 + r] = total;
+          cut_here = true;
+          if (r == 0)
+            ka.fix[cta] = make_int2(item, static_cast<int>((end * f.C - 1) / f.U));
+        } else {
+          ka.head[cta * 128 + r] = total;
         }
       }
-      total += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+      start = end;
+      ++part;
     }
-    if (ok && key_ok) {
-      if (ka.splits > 1) {
-        ka.part[(static_cast<int64_t>(sp) * bgs + bg) * a.Sk + j] = total;
-      } else {
-        const int64_t at = bg * a.Sk + j;
-        ka.w_out[at] = ka.w_in ? ka.w_in[at] + total : total;
-      }
-    }
+    if (n_iter > 0 && wg == 0 && r == 0 && !cut_here) ka.fix[cta] = make_int2(-1, 0);
   }
 
   tc_fence_before();
   __syncthreads();
   // Abort path: no warp issues anything past the barrier above.  Wait (with a limit) for the
   // copies and MMAs in flight before shared and tensor memory are released.
-  if (ctl->abort && n_iter > 0) {
+  if (ctl->abort) {
     if (warp == 0 && lane == 0) {
-      mbar_wait_limited(BAR(kBK), 0);
-      for (int it = max(0, issued - C::kStages); it < issued; ++it)
-        mbar_wait_limited(BAR(kBQF + it % C::kStages), (it / C::kStages) & 1);
+      for (int k = max(0, issued_k - C::kKStages); k < issued_k; ++k)
+        mbar_wait_limited(BAR(kBKF + k % C::kKStages), (k / C::kKStages) & 1);
+      for (int it = max(0, issued_q - C::kQStages); it < issued_q; ++it)
+        mbar_wait_limited(BAR(kBQF + it % C::kQStages), (it / C::kQStages) & 1);
     }
     if (warp == 1) {
       tc_fence_after();
@@ -323,38 +446,34 @@ __global__ void __launch_bounds__(192, Cfg<DQK>::kCtas)
   }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-// w_out = w_in + the parts in order
-__global__ void __launch_bounds__(256) key_weights_sum_kernel(const float* __restrict__ part,
-                                                              const float* w_in, float* w_out,
-                                                              int64_t n, int splits) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.f;
-  for (int k = 0; k < splits; ++k) s += part[k * n + i];
-  w_out[i] = w_in ? w_in[i] + s : s;
-}
-
-// CTAs over which the queries of one key tile are split: enough to fill the SMs (one wave),
-// at least four steps each.
-static int splits_of(const sparse_attn_params* p, int sms) {
-  const int64_t tn = (p->Sk + 127) / 128, tm = (p->Sq + 127) / 128;
-  const int64_t ctas = tn * p->B * p->HK;
-  const int64_t room = static_cast<int64_t>(sms) * (p->Dqk == 256 ? 1 : 2);
-  const int64_t steps = p->HQ / p->HK * tm * (p->Dqk <= 128 ? 1 : 2);
-  const int64_t s = min64(room / ctas, steps / 4);
-  return static_cast<int>(max64(1, min64(s, 64)));
-}
-
-static int sm_count() {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  (void)cudaGetLastError();
-  return sms;
+// Blocks c < C add the parts of the item that begins in CTA c and is cut; the others store the
+// items that no query sees (32 items each).
+__global__ void __launch_bounds__(128) key_weights_join_kernel(const Args ka) {
+  const AttnArgs& a = ka.t;
+  const int r = threadIdx.x, c = blockIdx.x;
+  auto store = [&](int item, float sum) {
+    const int bg = item / a.Tn;
+    const int64_t j = static_cast<int64_t>(item - bg * a.Tn) * 128 + r;
+    if (j >= a.Sk) return;
+    const int64_t at = static_cast<int64_t>(bg) * a.Sk + j;
+    ka.w_out[at] = ka.w_in ? ka.w_in[at] + sum : sum;
+  };
+  if (c < ka.C) {
+    const int2 fx = ka.fix[c];
+    if (fx.x < 0) return;
+    float sum = ka.tail[c * 128 + r];
+    for (int k = c + 1; k <= fx.y; ++k) sum += ka.head[k * 128 + r];
+    store(fx.x, sum);
+    return;
+  }
+  const int i0 = (c - ka.C) * 32;
+  for (int i = i0; i < min(i0 + 32, ka.items); ++i)
+    if (__ldg(a.tcnt + 2 * static_cast<int64_t>(i)) + __ldg(a.tcnt + 2 * static_cast<int64_t>(i) + 1) == 0)
+      store(i, 0.f);
 }
 
 template <int DQK>
@@ -367,8 +486,7 @@ static int launch(const Args& a, const CUtensorMap& mq, const CUtensorMap& mk, c
                       "key weights smem attribute");
   });
   if (rc) return rc;
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.t.Tn) * a.t.B * a.t.HK * a.splits);
-  key_weights_kernel<DQK><<<grid, 192, C::kSmem, st>>>(mq, mk, a);
+  key_weights_kernel<DQK><<<a.C, kThreads, C::kSmem, st>>>(mq, mk, a);
   return check_launch("key weights kernel launch");
 }
 
@@ -380,8 +498,7 @@ using namespace sa;
 extern "C" size_t sparse_attn_key_weights_workspace_size(const sparse_attn_params* p) {
   if (!p || p->B <= 0 || p->HQ <= 0 || p->HK <= 0 || p->Sq <= 0 || p->Sk <= 0 || p->Dqk <= 0)
     return 0;
-  const int s = kweights::splits_of(p, kweights::sm_count());
-  return s > 1 ? sizeof(float) * static_cast<size_t>(s) * p->B * p->HK * static_cast<size_t>(p->Sk) : 0;
+  return kweights::kMaxCtas * (2 * 128 * sizeof(float) + sizeof(int2));
 }
 
 extern "C" int sparse_attn_key_weights(const sparse_attn_params* p, const float* weights,
@@ -396,28 +513,34 @@ extern "C" int sparse_attn_key_weights(const sparse_attn_params* p, const float*
   int rc = fill_args(&fake, &a.t, false);
   if (rc) return rc;
   if (!weights_out) return SA_ERR_INVALID;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t items = static_cast<int64_t>(p->B) * p->HK * a.t.Tn;
+  if (items * a.t.Tm > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
   const size_t need = sparse_attn_key_weights_workspace_size(p);
-  if (need && (!workspace || workspace_bytes < need ||
-               (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0))
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
     return SA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = check_stream_device(st);
   if (rc) return rc;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SA_ERR_CUDA;
   a.w_in = weights;
   a.w_out = weights_out;
-  a.splits = kweights::splits_of(p, kweights::sm_count());
-  a.part = static_cast<float*>(workspace);
-  if (static_cast<int64_t>(a.t.Tn) * p->B * p->HK * a.splits > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
+  a.head = static_cast<float*>(workspace);
+  a.tail = a.head + kweights::kMaxCtas * 128;
+  a.fix = reinterpret_cast<int2*>(a.tail + kweights::kMaxCtas * 128);
+  a.items = static_cast<int>(items);
+  a.C = sms < kweights::kMaxCtas ? sms : kweights::kMaxCtas;
+  a.G = p->HQ / p->HK;
   CUtensorMap mq, mk;
-  if (!make_map(&mq, p->q, p->Dqk, p->Sq, p->HQ, p->B, p->Dqk <= 128 ? 128 : 64)) return SA_ERR_CUDA;
+  if (!make_map(&mq, p->q, p->Dqk, p->Sq, p->HQ, p->B, 128)) return SA_ERR_CUDA;
   if (!make_map(&mk, p->k, p->Dqk, p->Sk, p->HK, p->B, 128)) return SA_ERR_CUDA;
   if (p->Dqk == 64) rc = kweights::launch<64>(a, mq, mk, st);
   else if (p->Dqk == 128) rc = kweights::launch<128>(a, mq, mk, st);
   else if (p->Dqk == 192) rc = kweights::launch<192>(a, mq, mk, st);
   else rc = kweights::launch<256>(a, mq, mk, st);
-  if (rc || a.splits == 1) return rc;
-  const int64_t n = static_cast<int64_t>(p->B) * p->HK * p->Sk;
-  kweights::key_weights_sum_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, st>>>(
-      a.part, weights, weights_out, n, a.splits);
-  return check_launch("key weights sum kernel launch");
+  if (rc) return rc;
+  kweights::key_weights_join_kernel<<<static_cast<unsigned>(a.C + (a.items + 31) / 32), 128, 0, st>>>(a);
+  return check_launch("key weights join kernel launch");
 }

@@ -79,18 +79,15 @@ def test_key_weights_refusals(lib):
     assert call(Dqk=96) == UNSUP
     assert call(q=0x1008) == _lib.SA_ERR_ALIGN
     assert lib.sparse_attn_key_weights(None, None, 0x9000, None, 0, None) == BAD
-    # one key tile per KV head and 2 x 2 tiles of queries: nothing to split
     p = _lib.ParamsStruct(0x1000, 0x1000, None, None, 0x1000, None, None, None, None, 1, 4, 2, 128,
                           128, 256, 256, 0.125, ctypes.pointer(s), None)
-    assert lib.sparse_attn_key_weights_workspace_size(ctypes.byref(p)) == 0
-    # 256 query tiles of four heads over one key tile are split: a workspace is required
-    s.Sq, s.Sk = 32768, 128
-    p.Sq, p.Sk = 32768, 128
     need = lib.sparse_attn_key_weights_workspace_size(ctypes.byref(p))
-    assert need > 0 and need % (2 * 128 * 4) == 0
-    assert lib.sparse_attn_key_weights(ctypes.byref(p), None, 0x9000, None, 0, None) == _lib.SA_ERR_WORKSPACE
-    assert lib.sparse_attn_key_weights(ctypes.byref(p), None, 0x9000, 0x2000, need - 1,
-                                       None) == _lib.SA_ERR_WORKSPACE
+    assert need > 0
+    for ws, n in ((None, 0), (0x2000, need - 1), (0x2008, need)):
+        assert lib.sparse_attn_key_weights(ctypes.byref(p), None, 0x9000, ws, n,
+                                           None) == _lib.SA_ERR_WORKSPACE
+    p.B = 0
+    assert lib.sparse_attn_key_weights_workspace_size(ctypes.byref(p)) == 0
 
 
 @pytest.mark.parametrize("kw,code", [
