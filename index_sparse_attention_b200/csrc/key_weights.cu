@@ -15,40 +15,107 @@
 // of a CTA's range can be cut items, whose parts go to the workspace and are added by a second
 // kernel in CTA order.
 //   warp 0     TMA: an item's K tile and the Q tiles, several stages deep;
-//   warp 1     tcgen05.mma S^T = K Q^T into one of four TMEM buffers;
-//   warps 2-9  two warpgroups that take the units in turn (thread = key row):
-//              exp2(S^T scale log2e - lse log2e) summed over the 128 queries.  A unit's lse
-//              values (one per thread, fetched a unit ahead) pass through shared memory; the
-//              presence words of index mode are transposed across the warp.  Each unit is summed
-//              on its own before it joins the running sum, so that long query ranges do not lose
-//              low bits.
+//   warp 1     tcgen05.mma S^T = K Q^T into one of two to four TMEM buffers;
+//   two to four warpgroups that take the units in turn (thread = key row):
+//              exp2(S^T scale log2e - lse log2e) summed over the 128 queries.  The presence
+//              words of index mode are transposed across the warp, once for all heads of a
+//              tile.  Each unit is summed on its own before it joins the running sum, so that
+//              long query ranges do not lose low bits.
+//   the last warp feeds the units' lse values and list entries through a ring in shared memory.
 // Every mbarrier wait is bounded (sa_device.cuh).
+#include <type_traits>
+
 #include "sa_device.cuh"
 #include "sa_kernels.h"
 
 namespace sa {
 namespace kweights {
 
-constexpr int kThreads = 320;
+constexpr int kPoly = 0;                          // of eight exponentials, by polynomial
+constexpr int kRing = 8;                          // units the feeding warp can be ahead
 constexpr int kMaxCtas = 256;
 
 template <int DQK>
 struct Cfg {
   static constexpr int kKStages = DQK <= 128 ? 2 : 1;
-  static constexpr int kQStages = DQK == 64 ? 6 : DQK == 128 ? 4 : DQK == 192 ? 3 : 2;
+  // Q stages and TMEM S buffers: unit `it` uses stage and buffer it % kStages, so that one
+  // barrier tells the MMA warp that both are ready and one commit tells the producer and the
+  // epilogue that the MMAs are done (each wait costs the MMA warp 100 cycles even when the
+  // barrier is ready, each commit 50, and MMAs do not queue up behind them: with separate
+  // barriers a unit took 1000 cycles at head dim 128 for 545 cycles of MMAs)
+  static constexpr int kStages = DQK <= 128 ? 4 : DQK == 192 ? 3 : 2;
+  // Epilogue warpgroups: group it % kGroups reads unit `it`.  As many as there are buffers, so
+  // that a group waits on the barriers of its own buffer only and sees every phase of them (a
+  // wait by parity that comes two phases early is let through).
+  static constexpr int kGroups = kStages;
+  static constexpr int kFeed = 2 + 4 * kGroups;   // the feeding warp
+  static constexpr int kThreads = 32 * (kFeed + 1);
   static constexpr int kPanel = 128 * 128;  // 64 columns x 128 rows
   static constexpr int kTile = 128 * DQK * 2;
   static constexpr int kQOff = kKStages * kTile;
-  static constexpr int kLOff = kQOff + kQStages * kTile;  // lse [2 warpgroups][2][128]
-  static constexpr int kXOff = kLOff + 2 * 2 * 128 * 4;   // part sums of warpgroup 1, [2][128]
-  static constexpr int kFindOff = kXOff + 2 * 128 * 4;
+  static constexpr int kLOff = kQOff + kStages * kTile;  // per ring slot: -lse [128] (log2 units)
+  static constexpr int kDOff = kLOff + kRing * 128 * 4;   // per ring slot: query tile, list entry
+  static constexpr int kXOff = kDOff + kRing * 8;         // part sums, [2][kGroups - 1][128]
+  static constexpr int kFindOff = kXOff + 2 * (kGroups - 1) * 128 * 4;
   static constexpr int kBarOff = kFindOff + 80 * 4;
-  static constexpr int kSmem = kBarOff + 256 + 1024;
+  static constexpr int kSmem = kBarOff + 384 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
-enum : int { kBKF = 0, kBKE = 2, kBQF = 4, kBQE = 10, kBSF = 16, kBSE = 20, kBDrain = 24,
-             kNumBars = 25 };
+// Two fp32 values in one 64-bit register: one instruction does both lanes' operation.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // (a NaN stays one)
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 2^t as a mantissa p and a power of two s, without the special-function unit: t = n + f with n
+// the nearest integer (by adding and taking away 1.5 * 2^23), p a polynomial of degree 5 in f
+// (the minimax fit of 2^f over [-1/2, 1/2] in relative error by Remez exchange: 7.5e-8, 2.1e-7
+// with fp32 rounding), s = 2^n from the low bits of the shifted sum.  For t <= 127; below 2^-126
+// s is 0, as the unit flushes.  A NaN comes out as one (p is NaN).
+__device__ __forceinline__ void exp2_poly(uint64_t t2, uint64_t& p2, uint64_t& s2) {
+  const float2 t = unpack2(t2);
+  const uint64_t tc = pack2(max_nan(t.x, -127.f), max_nan(t.y, -127.f));
+  const uint64_t shift = pack2(12582912.f, 12582912.f);
+  const uint64_t tm = add2(tc, shift);
+  const uint64_t n = add2(tm, pack2(-12582912.f, -12582912.f));
+  const uint64_t f = fma2(n, pack2(-1.f, -1.f), tc);
+  auto c2 = [](float c) { return pack2(c, c); };
+  uint64_t p = fma2(c2(0.0013276472454890609f), f, c2(0.009675540961325169f));
+  p = fma2(p, f, c2(0.05550713092088699f));
+  p = fma2(p, f, c2(0.24022120237350464f));
+  p = fma2(p, f, c2(0.6931469440460205f));
+  p2 = fma2(p, f, c2(1.0000001192092896f));
+  const float2 m = unpack2(tm);
+  s2 = pack2(__uint_as_float((__float_as_uint(m.x) << 23) + 0x3F800000u),
+             __uint_as_float((__float_as_uint(m.y) << 23) + 0x3F800000u));
+}
+
+// kBFull: a unit's Q tile has landed (the producer) and its S buffer has been read (the 128
+// threads that read the unit kStages before); kBDone: its MMAs are done.
+enum : int { kBKF = 0, kBKE = 2, kBFull = 4, kBDone = 8, kBDrain = 12, kBRF = 13,
+             kBRE = kBRF + kRing, kNumBars = kBRE + kRing };
 
 struct Args {
   AttnArgs t;
@@ -61,37 +128,58 @@ struct Args {
   int items, C, G;
 };
 
-// Place of a unit: item (key tile of a KV head), list entry, head of the group.
-struct Cursor {
-  int item, n, n_full;  // list entries of the item (> 0), the full ones
-  int k, hh;
-  int tile, tile_next;  // list entries k and k + 1
+// The units of one item that a CTA takes.  Every value is broadcast from lane 0, so that the
+// compiler keeps them, and the descriptors and coordinates made from them, in uniform registers
+// (a tcgen05.mma or TMA whose operands have to be moved there first waits for each move).
+struct Part {
+  int item, n, n_full;  // list entries of the item, the full ones
+  int nt, b, h0;        // key tile, batch, first query head of the item
+  int k, hh;            // list entry and head of the first unit
+  int units;            // taken by this CTA
   const int32_t* list;
-  __device__ __forceinline__ void open(const Args& a, int it, int kk) {
-    item = it;
-    n_full = __ldg(a.t.tcnt + 2 * static_cast<int64_t>(it));
-    n = n_full + __ldg(a.t.tcnt + 2 * static_cast<int64_t>(it) + 1);
-    list = a.t.tidx + static_cast<int64_t>(it) * a.t.Tm;
-    k = kk;
-    if (kk < n) {
-      tile = __ldg(list + kk);
-      tile_next = kk + 1 < n ? __ldg(list + kk + 1) : 0;
-    }
+  __device__ __forceinline__ void open(const Args& a, int it, int64_t skip, int left) {
+    item = __shfl_sync(0xFFFFFFFFu, it, 0);
+    const int full = __ldg(a.t.tcnt + 2 * static_cast<int64_t>(item));
+    const int all = full + __ldg(a.t.tcnt + 2 * static_cast<int64_t>(item) + 1);
+    n_full = __shfl_sync(0xFFFFFFFFu, full, 0);
+    n = __shfl_sync(0xFFFFFFFFu, all, 0);
+    list = a.t.tidx + static_cast<int64_t>(item) * a.t.Tm;
+    const int bg = item / a.t.Tn;
+    nt = item - bg * a.t.Tn;
+    b = bg / a.t.HK;
+    h0 = (bg - b * a.t.HK) * a.G;
+    const int64_t most = static_cast<int64_t>(n) * a.G - skip;
+    units = static_cast<int>(min64(most, left));
+    k = static_cast<int>(skip / a.G);
+    hh = static_cast<int>(skip - static_cast<int64_t>(k) * a.G);
+    units = __shfl_sync(0xFFFFFFFFu, units, 0);
+    k = __shfl_sync(0xFFFFFFFFu, k, 0);
+    hh = __shfl_sync(0xFFFFFFFFu, hh, 0);
   }
-  // to the next unit; false past the last item
-  __device__ __forceinline__ bool next(const Args& a) {
-    if (++hh < a.G) return true;
-    hh = 0;
-    if (++k < n) {
-      tile = tile_next;
-      tile_next = k + 1 < n ? __ldg(list + k + 1) : 0;
-      return true;
+  // the next item with units (there is one)
+  __device__ __forceinline__ void next(const Args& a, int left) {
+    int i = item;
+    do {
+      ++i;
+      open(a, i, 0, left);
+    } while (n == 0);
+  }
+};
+
+// The query tiles of a part in the order of its units, 32 list entries at a time (a warp holds
+// one per lane).
+struct Tiles {
+  int base, mine;
+  __device__ __forceinline__ void start(const Part& p, int lane) {
+    base = p.k;
+    mine = base + lane < p.n ? __ldg(p.list + base + lane) : 0;
+  }
+  __device__ __forceinline__ int at(const Part& p, int k, int lane) {
+    if (k - base == 32) {
+      base = k;
+      mine = base + lane < p.n ? __ldg(p.list + base + lane) : 0;
     }
-    for (int i = item + 1; i < a.items; ++i) {
-      open(a, i, 0);
-      if (n > 0) return true;
-    }
-    return false;
+    return __shfl_sync(0xFFFFFFFFu, mine, k - base);
   }
 };
 
@@ -101,6 +189,7 @@ struct Found {
   int64_t U, u0, u1, off;
   int item, C;
 };
+template <int kThreads>
 __device__ __forceinline__ Found find_range(const Args& a, int c, int* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.items + kThreads - 1) / kThreads;
@@ -151,10 +240,11 @@ __device__ __forceinline__ Found find_range(const Args& a, int c, int* sh) {
 }
 
 template <int DQK>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const Args ka) {
   using C = Cfg<DQK>;
+  constexpr int kGroups = C::kGroups;
   const AttnArgs& a = ka.t;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -168,7 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cta = blockIdx.x;
 
   if (threadIdx.x == 0) {
-    for (int k = 0; k < kNumBars; ++k) mbar_init(BAR(k), k >= kBSE && k < kBSE + 4 ? 128 : 1);
+    for (int k = 0; k < kNumBars; ++k)
+      mbar_init(BAR(k), k >= kBRE                          ? 128
+                        : k >= kBRF                        ? 32
+                        : k >= kBFull && k < kBFull + 4    ? 129
+                                                           : 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -177,54 +271,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Found f = find_range(ka, cta, reinterpret_cast<int*>(smem + C::kFindOff));
+  const Found f = find_range<C::kThreads>(ka, cta, reinterpret_cast<int*>(smem + C::kFindOff));
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  const int n_iter = static_cast<int>(f.u1 - f.u0);
+  const int n_iter = __shfl_sync(0xFFFFFFFFu, static_cast<int>(f.u1 - f.u0), 0);
   if (n_iter == 0 && threadIdx.x == 0) ka.fix[cta] = make_int2(-1, 0);
-  Cursor cur{};
-  if (n_iter > 0) {
-    const int64_t r = f.u0 - f.off;
-    cur.open(ka, f.item, static_cast<int>(r / ka.G));
-    cur.hh = static_cast<int>(r - static_cast<int64_t>(cur.k) * ka.G);
-  }
+  Part p{};
+  if (n_iter > 0) p.open(ka, f.item, f.u0 - f.off, n_iter);
   int issued_q = 0, issued_k = 0;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
-    int item = -1;
-    for (int it = 0; it < n_iter; ++it) {
-      const int bg = cur.item / a.Tn, b = bg / a.HK, g = bg - b * a.HK;
-      if (cur.item != item) {
-        item = cur.item;
-        const int ks = issued_k % C::kKStages, ku = issued_k / C::kKStages;
-        if (!warp_wait(BAR(kBKE + ks), (ku & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(BAR(kBKF + ks), C::kTile);
-          for (int c = 0; c < DQK / 64; ++c)
-            tma_load_4d(sbase + ks * C::kTile + c * C::kPanel, &tm_k, BAR(kBKF + ks), c * 64,
-                        (item - bg * a.Tn) * 128, g, b);
-        }
-        __syncwarp();
-        ++issued_k;
-      }
-      const int st = it % C::kQStages, u = it / C::kQStages;
-      if (!warp_wait(BAR(kBQE + st), (u & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
-      const int m0 = __shfl_sync(0xFFFFFFFFu, cur.tile, 0) * 128;
+    bool ok = true;
+    for (int it = 0; ok && it < n_iter;) {
+      const int ks = issued_k % C::kKStages, ku = issued_k / C::kKStages;
+      if (!warp_wait(BAR(kBKE + ks), (ku & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(BAR(kBQF + st), C::kTile);
+        mbar_arrive_expect_tx(BAR(kBKF + ks), C::kTile);
         for (int c = 0; c < DQK / 64; ++c)
-          tma_load_4d(sbase + C::kQOff + st * C::kTile + c * C::kPanel, &tm_q, BAR(kBQF + st),
-                      c * 64, m0, g * ka.G + cur.hh, b);
+          tma_load_4d(sbase + ks * C::kTile + c * C::kPanel, &tm_k, BAR(kBKF + ks), c * 64,
+                      p.nt * 128, p.h0 / ka.G, p.b);
       }
       __syncwarp();
-      issued_q = it + 1;
-      if (it + 1 < n_iter) cur.next(ka);
+      ++issued_k;
+      Tiles tiles;
+      tiles.start(p, lane);
+      int k = p.k, hh = p.hh;
+      for (int u = 0; u < p.units; ++u, ++it) {
+        const int m0 = tiles.at(p, k, lane) * 128;
+        const int st = it % C::kStages, su = it / C::kStages;
+        if (!warp_wait(BAR(kBDone + st), (su & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          mbar_arrive_expect_tx(BAR(kBFull + st), C::kTile);
+          for (int c = 0; c < DQK / 64; ++c)
+            tma_load_4d(sbase + C::kQOff + st * C::kTile + c * C::kPanel, &tm_q, BAR(kBFull + st),
+                        c * 64, m0, p.h0 + hh, p.b);
+        }
+        __syncwarp();
+        issued_q = it + 1;
+        if (++hh == ka.G) {
+          hh = 0;
+          ++k;
+        }
+      }
+      if (ok && it < n_iter) p.next(ka, n_iter - it);
     }
     // the last arrivals on the stages' barriers have landed before the CTA may leave
     if (issued_q == n_iter) {
-      for (int it = max(0, n_iter - C::kQStages); it < n_iter; ++it)
-        if (!warp_wait(BAR(kBQE + it % C::kQStages), (it / C::kQStages) & 1, ctl, a.status,
+      for (int it = max(0, n_iter - C::kStages); it < n_iter; ++it)
+        if (!warp_wait(BAR(kBDone + it % C::kStages), (it / C::kStages) & 1, ctl, a.status,
                        a.wait_limit_ns))
           break;
       for (int k = max(0, issued_k - C::kKStages); k < issued_k; ++k)
@@ -235,172 +333,207 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc = idesc_bf16(128, 128, 0, 0);
-    int item = -1, part = -1;
-    for (int it = 0; it < n_iter; ++it) {
-      if (cur.item != item) {
-        item = cur.item;
-        ++part;
-        if (!warp_wait(BAR(kBKF + part % C::kKStages), (part / C::kKStages) & 1, ctl, a.status,
-                       a.wait_limit_ns))
-          break;
-      }
-      const int st = it % C::kQStages, u = it / C::kQStages, sb = it & 3;
-      if (!warp_wait(BAR(kBQF + st), u & 1, ctl, a.status, a.wait_limit_ns)) break;
-      if (!warp_wait(BAR(kBSE + sb), ((it >> 2) & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
-      tc_fence_after();
-      const bool more = it + 1 < n_iter;
-      if (more) cur.next(ka);
+    int part = 0;
+    bool ok = true;
+    for (int it = 0; ok && it < n_iter; ++part) {
       const int ks = part % C::kKStages;
+      if (!warp_wait(BAR(kBKF + ks), (part / C::kKStages) & 1, ctl, a.status, a.wait_limit_ns)) break;
       const uint64_t kd = sw128_desc(sbase + ks * C::kTile, 16, 1024);
-      const uint64_t qd = sw128_desc(sbase + C::kQOff + st * C::kTile, 16, 1024);
-      if (elect_one()) {
+      for (int u = 0; u < p.units; ++u, ++it) {
+        const int st = it % C::kStages, su = it / C::kStages;
+        ok = warp_wait(BAR(kBFull + st), su & 1, ctl, a.status, a.wait_limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t qd = sw128_desc(sbase + C::kQOff + st * C::kTile, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DQK / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
-          umma_ss(tmem + sb * 128, kd + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < DQK / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4;
+            umma_ss(tmem + st * 128, kd + off, qd + off, idesc, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(BAR(kBDone + st));
+          if (u + 1 == p.units) umma_commit(BAR(kBKE + ks));
         }
-        umma_commit(BAR(kBSF + sb));
-        umma_commit(BAR(kBQE + st));
-        if (!more || cur.item != item) umma_commit(BAR(kBKE + ks));
+        __syncwarp();
       }
-      __syncwarp();
+      if (ok && it < n_iter) p.next(ka, n_iter - it);
+    }
+  } else if (warp == C::kFeed) {
+    // ---------------------------------------------------------------- feeding warp
+    // Four units at a time: their query tiles, list entries and lse values (in log2 units)
+    // into ring slots; a row past Sq, or one that saw no key, adds nothing: exp2(-inf).
+    float* lse_s = reinterpret_cast<float*>(smem + C::kLOff);
+    int2* desc = reinterpret_cast<int2*>(smem + C::kDOff);
+    bool ok = true;
+    Tiles tiles;
+    tiles.start(p, lane);
+    int k = p.k, hh = p.hh, left = p.units;
+    for (int it = 0; ok && it < n_iter; it += 4) {
+      float l[4][4];
+      int2 d[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (it + x >= n_iter) break;
+        const int tile = tiles.at(p, k, lane);
+        d[x] = make_int2(tile, k);
+        const float* row = a.lse + (static_cast<int64_t>(p.b) * a.HQ + p.h0 + hh) * a.Sq;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int i = tile * 128 + 32 * y + lane;
+          l[x][y] = i < a.Sq ? __ldg(row + i) : -INFINITY;
+        }
+        if (++hh == ka.G) {
+          hh = 0;
+          ++k;
+        }
+        if (--left == 0 && it + x + 1 < n_iter) {
+          p.next(ka, n_iter - (it + x + 1));
+          tiles.start(p, lane);
+          k = p.k;
+          hh = p.hh;
+          left = p.units;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (it + x >= n_iter) break;
+        const int slot = (it + x) % kRing, u = (it + x) / kRing;
+        ok = ok && warp_wait(BAR(kBRE + slot), (u & 1) ^ 1, ctl, a.status, a.wait_limit_ns);
+        if (!ok) break;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          lse_s[slot * 128 + 32 * y + lane] =
+              l[x][y] == -INFINITY ? -INFINITY : l[x][y] * -1.4426950408889634f;
+        if (lane == 0) desc[slot] = d[x];
+        mbar_arrive(BAR(kBRF + slot));
+      }
     }
   } else {
     // ---------------------------------------------------------------- exponentials and sums
     const int quarter = warp & 3, wg = (warp - 2) >> 2;
-    const int r = quarter * 32 + lane;       // key row of the item = TMEM lane
-    const int tq = (threadIdx.x - 64) & 127;  // the query of a unit whose lse this thread fetches
+    const int r = quarter * 32 + lane;  // key row of the item = TMEM lane
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    float* lbuf = reinterpret_cast<float*>(smem + C::kLOff) + wg * 256;
+    const float* lse_s = reinterpret_cast<const float*>(smem + C::kLOff);
+    const int2* desc = reinterpret_cast<const int2*>(smem + C::kDOff);
     float* xch = reinterpret_cast<float*>(smem + C::kXOff);
     const float sc = a.scale_log2;
-    // `nxt` runs one of this warpgroup's units ahead of `cur` and fetches its lse
-    float l_nxt = 0.f;
-    Cursor nxt = cur;
-    bool more = n_iter > 0;   // nxt is a unit of this CTA
-    int it_n = 0;             // and its number
-    auto fetch = [&]() {
-      if (!more) return;
-      const int bg = nxt.item / a.Tn, b = bg / a.HK, g = bg - b * a.HK;
-      const int64_t i = static_cast<int64_t>(nxt.tile) * 128 + tq;
-      // (a row past Sq, or one that saw no key, adds nothing: exp2(-inf))
-      float l = -INFINITY;
-      if (i < a.Sq)
-        l = __ldg(a.lse + (static_cast<int64_t>(b) * a.HQ + g * ka.G + nxt.hh) * a.Sq + i);
-      l_nxt = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-    };
-    auto advance = [&](int by) {
-      for (int x = 0; x < by && more; ++x) {
-        ++it_n;
-        more = it_n < n_iter && nxt.next(ka);
-      }
-    };
-    advance(wg);
-    fetch();
+    if (wg == 0 && n_iter > 0)  // every S buffer is free at first
+      for (int k = 0; k < C::kStages; ++k) mbar_arrive(BAR(kBFull + k));
     uint32_t cm[4] = {0u, 0u, 0u, 0u};  // which of the tile's queries see this key
-    int cm_item = -1, cm_k = -1;
-    bool ok = true;
-    int part = 0;
-    int it = 0;
+    bool ok = true, cut_here = false;
+    int part = 0, it = wg;  // this warpgroup's next unit
     int64_t start = f.off;  // first unit of the item
-    bool cut_here = false;
-    while (it < n_iter) {
+    int it_end = 0;
+    while (it_end < n_iter) {
       // ------------------------------------------------------------ one part: units of an item
-      const int item = cur.item;
-      const int64_t end = start + static_cast<int64_t>(cur.n) * ka.G;
-      const int it_end = static_cast<int>(min64(end, f.u1) - f.u0);
-      const int bg = item / a.Tn, nt = item - bg * a.Tn;
+      const int64_t end = start + static_cast<int64_t>(p.n) * ka.G;
+      it_end += p.units;
+      const int item = p.item, n_full = p.n_full, nt = p.nt, bg = p.item / a.Tn;
       const int64_t j = static_cast<int64_t>(nt) * 128 + r;
       const bool key_ok = j < a.Sk;
       float total = 0.f;
-      for (; it < it_end; ++it) {
-        if ((it & 1) == wg) {
-          const int sb = it & 3;
-          float* ls = lbuf + ((it >> 1) & 1) * 128;
-          ls[tq] = l_nxt;
-          advance(2);
-          fetch();
-          const bool partial = cur.k >= cur.n_full;
-          if (partial && (cm_k != cur.k || cm_item != item)) {
-            cm_k = cur.k;
-            cm_item = item;
+      int cm_k = -1;
+      for (; it < it_end; it += kGroups) {
+        const int sb = it % C::kStages, slot = it % kRing;
+        // (a warp whose wait gave up goes on without work, so that the groups still meet)
+        if (ok)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBRF + slot), (it / kRing) & 1, ctl, a.status,
+                                                 a.wait_limit_ns));
+        if (!ok) continue;
+        const int2 d = desc[slot];
+        const bool partial = d.y >= n_full;
+        if (partial && cm_k != d.y) {
+          cm_k = d.y;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int64_t q0 = static_cast<int64_t>(cur.tile) * 128 + 32 * c;
-              uint32_t x = key_ok ? 0xFFFFFFFFu : 0u;
-              if (a.causal) {  // i >= j
-                const int64_t lo = j - q0;
-                x &= lo <= 0 ? 0xFFFFFFFFu : (lo >= 32 ? 0u : (0xFFFFFFFFu << lo));
-              }
-              if (a.mode == SA_MODE_BLOCK && a.bs == 64 && key_ok) {
-                const int64_t mb = q0 / 64;
-                if (!(mb < a.Mb &&
-                      __ldg(a.mask + (static_cast<int64_t>(bg) * a.Mb + mb) * a.Nb + j / 64) != 0))
-                  x = 0u;
-              } else if (a.mode == SA_MODE_INDEX) {
-                // lane L loads the presence word of query q0 + L over this warp's 32 keys; the
-                // transpose leaves in lane L the word of key L over the 32 queries
-                const int64_t i = q0 + lane;
-                const int w = nt * 4 + quarter;
-                const uint32_t bits =
-                    (i < a.Sq && w < a.W)
-                        ? __ldg(a.bitmap + (static_cast<int64_t>(bg) * a.Sq + i) * a.W + w)
-                        : 0u;
-                x &= warp_transpose32(bits, lane);
-              }
-              cm[c] = x;
+          for (int c = 0; c < 4; ++c) {
+            const int64_t q0 = static_cast<int64_t>(d.x) * 128 + 32 * c;
+            uint32_t x = key_ok ? 0xFFFFFFFFu : 0u;
+            if (a.causal) {  // i >= j
+              const int64_t lo = j - q0;
+              x &= lo <= 0 ? 0xFFFFFFFFu : (lo >= 32 ? 0u : (0xFFFFFFFFu << lo));
             }
-          }
-          if (ok)
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBSF + sb), (it >> 2) & 1, ctl, a.status,
-                                                   a.wait_limit_ns));
-          named_bar_sync(1 + wg, 128);  // the unit's lse values are in shared memory
-          if (ok) {
-            tc_fence_after();
-            const float4* ls4 = reinterpret_cast<const float4*>(ls);
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_ld32(tl + sb * 128 + 32 * c, s);
-              tmem_wait_ld();
-              if (c == 3) {  // every column is read: the buffer is free
-                tc_fence_before();
-                mbar_arrive(BAR(kBSE + sb));
-              }
-              if (!partial) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 l = ls4[8 * c + e];
-                  ps[0] += ex2(fmaf(__uint_as_float(s[4 * e]), sc, -l.x));
-                  ps[1] += ex2(fmaf(__uint_as_float(s[4 * e + 1]), sc, -l.y));
-                  ps[2] += ex2(fmaf(__uint_as_float(s[4 * e + 2]), sc, -l.z));
-                  ps[3] += ex2(fmaf(__uint_as_float(s[4 * e + 3]), sc, -l.w));
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 l = ls4[8 * c + e];
-                  const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                  for (int t = 0; t < 4; ++t) {
-                    const float p = ex2(fmaf(__uint_as_float(s[4 * e + t]), sc, -lv[t]));
-                    ps[t] += ((cm[c] >> (4 * e + t)) & 1u) ? p : 0.f;
-                  }
-                }
-              }
+            if (a.mode == SA_MODE_BLOCK && a.bs == 64 && key_ok) {
+              const int64_t mb = q0 / 64;
+              if (!(mb < a.Mb &&
+                    __ldg(a.mask + (static_cast<int64_t>(bg) * a.Mb + mb) * a.Nb + j / 64) != 0))
+                x = 0u;
+            } else if (a.mode == SA_MODE_INDEX) {
+              // lane L loads the presence word of query q0 + L over this warp's 32 keys; the
+              // transpose leaves in lane L the word of key L over the 32 queries
+              const int64_t i = q0 + lane;
+              const int w = nt * 4 + quarter;
+              const uint32_t bits =
+                  (i < a.Sq && w < a.W)
+                      ? __ldg(a.bitmap + (static_cast<int64_t>(bg) * a.Sq + i) * a.W + w)
+                      : 0u;
+              x &= warp_transpose32(bits, lane);
             }
-            total += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+            cm[c] = x;
           }
         }
-        if (it + 1 < n_iter) cur.next(ka);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBDone + sb), (it / C::kStages) & 1, ctl,
+                                               a.status, a.wait_limit_ns));
+        if (!ok) continue;
+        tc_fence_after();
+        const ulonglong2* ls2 = reinterpret_cast<const ulonglong2*>(lse_s + slot * 128);
+        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of sums
+        auto sweep = [&](auto masked) {
+          constexpr bool kMasked = decltype(masked)::value;
+          uint32_t buf[2][16];
+          tmem_ld16(tl + sb * 128, buf[0]);
+  #pragma unroll
+          for (int c = 0; c < 8; ++c) {  // 16 columns; the next ones are on their way meanwhile
+            tmem_wait_ld();
+            if (c < 7) tmem_ld16(tl + sb * 128 + 16 * (c + 1), buf[(c + 1) & 1]);
+            else {  // every column is read: the buffer is free
+              tc_fence_before();
+              mbar_arrive(BAR(kBFull + sb));
+            }
+            const uint32_t* s = buf[c & 1];
+  #pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const ulonglong2 l = ls2[4 * c + (e >> 1)];
+              const uint64_t t2 = fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                       pack2(sc, sc), (e & 1) ? l.y : l.x);
+              // kPoly of every eight pairs go through the fused multiply-add pipe, the others
+              // through the special-function unit
+              const bool poly = e * kPoly / 8 != (e + 1) * kPoly / 8;
+              const uint32_t bits = cm[c >> 1] >> (16 * (c & 1) + 2 * e);
+              if (poly) {
+                uint64_t p2, s2;
+                exp2_poly(t2, p2, s2);
+                if constexpr (!kMasked) {
+                  ps[e & 3] = fma2(p2, s2, ps[e & 3]);
+                } else {
+                  const float2 pv = unpack2(p2), sv = unpack2(s2);
+                  ps[e & 3] = add2(ps[e & 3], pack2((bits & 1u) ? pv.x * sv.x : 0.f,
+                                                    (bits & 2u) ? pv.y * sv.y : 0.f));
+                }
+              } else {
+                const float2 t = unpack2(t2);
+                float p0 = ex2(t.x), p1 = ex2(t.y);
+                if constexpr (kMasked) {
+                  p0 = (bits & 1u) ? p0 : 0.f;
+                  p1 = (bits & 2u) ? p1 : 0.f;
+                }
+                ps[e & 3] = add2(ps[e & 3], pack2(p0, p1));
+              }
+            }
+          }
+        };
+        if (partial) sweep(std::true_type{});
+        else sweep(std::false_type{});
+        mbar_arrive(BAR(kBRE + slot));
+        const float2 sum = unpack2(add2(add2(ps[0], ps[1]), add2(ps[2], ps[3])));
+        total += sum.x + sum.y;
       }
       // ------------------------------------------------------------ the part's sum
-      float* xp = xch + (part & 1) * 128;
-      if (wg == 1) xp[r] = total;
-      named_bar_sync(3, 256);
+      float* xp = xch + (part & 1) * (kGroups - 1) * 128;
+      if (wg > 0) xp[(wg - 1) * 128 + r] = total;
+      named_bar_sync(1, 128 * kGroups);
       if (wg == 0) {
-        total += xp[r];
+#pragma unroll
+        for (int x = 0; x < kGroups - 1; ++x) total += xp[x * 128 + r];
         const bool begins = start >= f.u0, ends = end <= f.u1;
         if (begins && ends) {
           if (key_ok) {
@@ -418,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       start = end;
       ++part;
+      if (it_end < n_iter) p.next(ka, n_iter - it_end);
     }
     if (n_iter > 0 && wg == 0 && r == 0 && !cut_here) ka.fix[cta] = make_int2(-1, 0);
   }
@@ -430,8 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
       for (int k = max(0, issued_k - C::kKStages); k < issued_k; ++k)
         mbar_wait_limited(BAR(kBKF + k % C::kKStages), (k / C::kKStages) & 1);
-      for (int it = max(0, issued_q - C::kQStages); it < issued_q; ++it)
-        mbar_wait_limited(BAR(kBQF + it % C::kQStages), (it / C::kQStages) & 1);
+      // (a Q tile's barrier also counts its S buffer's readers, who may have left: its bytes
+      // are given 50 us instead, against a few for a load)
+      const uint64_t t0 = globaltimer_ns();
+      while (issued_q > 0 && globaltimer_ns() - t0 < 50000) __nanosleep(1000);
     }
     if (warp == 1) {
       tc_fence_after();
@@ -486,7 +622,7 @@ static int launch(const Args& a, const CUtensorMap& mq, const CUtensorMap& mk, c
                       "key weights smem attribute");
   });
   if (rc) return rc;
-  key_weights_kernel<DQK><<<a.C, kThreads, C::kSmem, st>>>(mq, mk, a);
+  key_weights_kernel<DQK><<<a.C, C::kThreads, C::kSmem, st>>>(mq, mk, a);
   return check_launch("key weights kernel launch");
 }
 

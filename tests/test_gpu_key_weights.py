@@ -31,6 +31,16 @@ CASES = [
     I.scaled(IDX, Sq=200, Sk=200, HQ=4, HK=2, Dqk=256, Dv=256, topk=40, name="index_d256"),
     I.scaled(W["long_causal_blocksparse_h16_s32768_d256"], Sq=600, Sk=600, HQ=4, HK=4, density=0.5,
              name="causal_d256"),
+    # many tiles for every SM
+    I.scaled(GQA, B=1, Sq=1400, Sk=1400, HQ=32, HK=4, density=0.7, name="many_tiles_d128"),
+    I.scaled(GQA, B=1, Sq=1409, Sk=1300, HQ=32, HK=4, Dqk=64, Dv=64, density=0.7,
+             name="many_tiles_d64"),
+    I.scaled(GQA, B=1, Sq=1400, Sk=1400, HQ=32, HK=4, Dqk=192, density=0.7,
+             name="many_tiles_d192"),
+    I.scaled(GQA, B=1, Sq=1400, Sk=1401, HQ=32, HK=8, Dqk=256, Dv=256, density=0.7, causal=False,
+             name="many_tiles_d256"),
+    I.scaled(IDX, Sq=1401, Sk=1401, HQ=32, HK=4, Dqk=128, topk=200, name="index_many_tiles_d128"),
+    I.scaled(IDX, Sq=1401, Sk=1401, HQ=32, HK=4, topk=200, name="index_many_tiles_d192"),
 ]
 
 
