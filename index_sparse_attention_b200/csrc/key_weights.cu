@@ -16,12 +16,20 @@
 // kernel in CTA order.
 //   warp 0     TMA: an item's K tile and the Q tiles, several stages deep;
 //   warp 1     tcgen05.mma S^T = K Q^T into one of two to four TMEM buffers;
-//   two to four warpgroups that take the units in turn (thread = key row):
-//              exp2(S^T scale log2e - lse log2e) summed over the 128 queries.  The presence
-//              words of index mode are transposed across the warp, once for all heads of a
-//              tile.  Each unit is summed on its own before it joins the running sum, so that
-//              long query ranges do not lose low bits.
-//   the last warp feeds the units' lse values and list entries through a ring in shared memory.
+//   warps 2-17 exp2(S^T scale log2e - lse log2e), summed: thread = key row, a quarter of the
+//              unit's 128 queries per warpgroup.  The presence words of index mode are
+//              transposed across the warp, once for all heads of a tile.  Each unit is summed
+//              on its own before it joins the running sum, so that long query ranges do not
+//              lose low bits.
+//   warp 18    feeds the units' lse values and list entries through shared memory.
+// What bounds it: the special-function unit.  A unit's 16384 exponentials take an SM 1024 cycles
+// (its MMAs 512 at head dim 128); measured 1360 cycles a unit on long prompts (107 us for the
+// causal prompt B=2 H=16 S=4096 D=128, 642 TFLOP/s of allowed pairs; 116 us for the index prompt
+// with 32 heads, S=4001, head dims 192/128).  Tried and slower: a unit per warpgroup (113 us;
+// a group stands idle while its buffer is refilled), eight warps with half a unit each and the
+// next half's TMEM loads in flight (130 us; the remaining latency of a unit is shared by fewer
+// warps), an eighth to a half of the exponentials by a polynomial of packed fused multiply-adds
+// (107 to 124 us: the warps are short of issue slots, not of that unit alone).
 // Every mbarrier wait is bounded (sa_device.cuh).
 #include <type_traits>
 
@@ -31,31 +39,26 @@
 namespace sa {
 namespace kweights {
 
-constexpr int kPoly = 0;                          // of eight exponentials, by polynomial
-constexpr int kRing = 8;                          // units the feeding warp can be ahead
+constexpr int kGroups = 4;                        // epilogue warpgroups
+constexpr int kFeed = 2 + 4 * kGroups;            // the feeding warp
+constexpr int kThreads = 32 * (kFeed + 1);
 constexpr int kMaxCtas = 256;
 
 template <int DQK>
 struct Cfg {
   static constexpr int kKStages = DQK <= 128 ? 2 : 1;
-  // Q stages and TMEM S buffers: unit `it` uses stage and buffer it % kStages, so that one
-  // barrier tells the MMA warp that both are ready and one commit tells the producer and the
-  // epilogue that the MMAs are done (each wait costs the MMA warp 100 cycles even when the
-  // barrier is ready, each commit 50, and MMAs do not queue up behind them: with separate
-  // barriers a unit took 1000 cycles at head dim 128 for 545 cycles of MMAs)
+  // Q stages and TMEM S buffers (and the lse slots): unit `it` uses number it % kStages of each,
+  // so that one barrier tells the MMA warp that all are ready and one tells the epilogue that
+  // its inputs are (each wait costs a warp 100 cycles even when the barrier is ready, each
+  // commit 50, and MMAs do not queue up behind them: with a barrier for each a unit took 1000
+  // cycles at head dim 128 for 545 cycles of MMAs)
   static constexpr int kStages = DQK <= 128 ? 4 : DQK == 192 ? 3 : 2;
-  // Epilogue warpgroups: group it % kGroups reads unit `it`.  As many as there are buffers, so
-  // that a group waits on the barriers of its own buffer only and sees every phase of them (a
-  // wait by parity that comes two phases early is let through).
-  static constexpr int kGroups = kStages;
-  static constexpr int kFeed = 2 + 4 * kGroups;   // the feeding warp
-  static constexpr int kThreads = 32 * (kFeed + 1);
   static constexpr int kPanel = 128 * 128;  // 64 columns x 128 rows
   static constexpr int kTile = 128 * DQK * 2;
   static constexpr int kQOff = kKStages * kTile;
-  static constexpr int kLOff = kQOff + kStages * kTile;  // per ring slot: -lse [128] (log2 units)
-  static constexpr int kDOff = kLOff + kRing * 128 * 4;   // per ring slot: query tile, list entry
-  static constexpr int kXOff = kDOff + kRing * 8;         // part sums, [2][kGroups - 1][128]
+  static constexpr int kLOff = kQOff + kStages * kTile;  // per slot: -lse [128] (log2 units)
+  static constexpr int kDOff = kLOff + kStages * 128 * 4;  // per slot: query tile, list entry
+  static constexpr int kXOff = kDOff + 4 * 8;             // part sums, [2][kGroups - 1][128]
   static constexpr int kFindOff = kXOff + 2 * (kGroups - 1) * 128 * 4;
   static constexpr int kBarOff = kFindOff + 80 * 4;
   static constexpr int kSmem = kBarOff + 384 + 1024;
@@ -83,39 +86,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {  // (a NaN stays one)
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-// 2^t as a mantissa p and a power of two s, without the special-function unit: t = n + f with n
-// the nearest integer (by adding and taking away 1.5 * 2^23), p a polynomial of degree 5 in f
-// (the minimax fit of 2^f over [-1/2, 1/2] in relative error by Remez exchange: 7.5e-8, 2.1e-7
-// with fp32 rounding), s = 2^n from the low bits of the shifted sum.  For t <= 127; below 2^-126
-// s is 0, as the unit flushes.  A NaN comes out as one (p is NaN).
-__device__ __forceinline__ void exp2_poly(uint64_t t2, uint64_t& p2, uint64_t& s2) {
-  const float2 t = unpack2(t2);
-  const uint64_t tc = pack2(max_nan(t.x, -127.f), max_nan(t.y, -127.f));
-  const uint64_t shift = pack2(12582912.f, 12582912.f);
-  const uint64_t tm = add2(tc, shift);
-  const uint64_t n = add2(tm, pack2(-12582912.f, -12582912.f));
-  const uint64_t f = fma2(n, pack2(-1.f, -1.f), tc);
-  auto c2 = [](float c) { return pack2(c, c); };
-  uint64_t p = fma2(c2(0.0013276472454890609f), f, c2(0.009675540961325169f));
-  p = fma2(p, f, c2(0.05550713092088699f));
-  p = fma2(p, f, c2(0.24022120237350464f));
-  p = fma2(p, f, c2(0.6931469440460205f));
-  p2 = fma2(p, f, c2(1.0000001192092896f));
-  const float2 m = unpack2(tm);
-  s2 = pack2(__uint_as_float((__float_as_uint(m.x) << 23) + 0x3F800000u),
-             __uint_as_float((__float_as_uint(m.y) << 23) + 0x3F800000u));
-}
-
-// kBFull: a unit's Q tile has landed (the producer) and its S buffer has been read (the 128
-// threads that read the unit kStages before); kBDone: its MMAs are done.
-enum : int { kBKF = 0, kBKE = 2, kBFull = 4, kBDone = 8, kBDrain = 12, kBRF = 13,
-             kBRE = kBRF + kRing, kNumBars = kBRE + kRing };
+// kBFull: a unit's Q tile has landed (the producer) and its S buffer and lse slot have been
+// read (by every epilogue warp, for the unit kStages before).  kBDone: its MMAs are done and its
+// lse slot is filled (the feeding warp).  Every waiter waits for every unit in turn: a wait by
+// parity that comes a phase early would be let through.
+enum : int { kBKF = 0, kBKE = 2, kBFull = 4, kBDone = 8, kBDrain = 12, kNumBars = 13 };
 
 struct Args {
   AttnArgs t;
@@ -189,7 +164,6 @@ struct Found {
   int64_t U, u0, u1, off;
   int item, C;
 };
-template <int kThreads>
 __device__ __forceinline__ Found find_range(const Args& a, int c, int* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.items + kThreads - 1) / kThreads;
@@ -240,11 +214,10 @@ __device__ __forceinline__ Found find_range(const Args& a, int c, int* sh) {
 }
 
 template <int DQK>
-__global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const Args ka) {
   using C = Cfg<DQK>;
-  constexpr int kGroups = C::kGroups;
   const AttnArgs& a = ka.t;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -259,10 +232,9 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int k = 0; k < kNumBars; ++k)
-      mbar_init(BAR(k), k >= kBRE                          ? 128
-                        : k >= kBRF                        ? 32
-                        : k >= kBFull && k < kBFull + 4    ? 129
-                                                           : 1);
+      mbar_init(BAR(k), k >= kBFull && k < kBFull + 4   ? 1 + 4 * kGroups
+                        : k >= kBDone && k < kBDone + 4 ? 2
+                                                        : 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -271,7 +243,7 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Found f = find_range<C::kThreads>(ka, cta, reinterpret_cast<int*>(smem + C::kFindOff));
+  const Found f = find_range(ka, cta, reinterpret_cast<int*>(smem + C::kFindOff));
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const int n_iter = __shfl_sync(0xFFFFFFFFu, static_cast<int>(f.u1 - f.u0), 0);
@@ -358,10 +330,10 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
       }
       if (ok && it < n_iter) p.next(ka, n_iter - it);
     }
-  } else if (warp == C::kFeed) {
+  } else if (warp == kFeed) {
     // ---------------------------------------------------------------- feeding warp
     // Four units at a time: their query tiles, list entries and lse values (in log2 units)
-    // into ring slots; a row past Sq, or one that saw no key, adds nothing: exp2(-inf).
+    // into the slots; a row past Sq, or one that saw no key, adds nothing: exp2(-inf).
     float* lse_s = reinterpret_cast<float*>(smem + C::kLOff);
     int2* desc = reinterpret_cast<int2*>(smem + C::kDOff);
     bool ok = true;
@@ -397,15 +369,16 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         if (it + x >= n_iter) break;
-        const int slot = (it + x) % kRing, u = (it + x) / kRing;
-        ok = ok && warp_wait(BAR(kBRE + slot), (u & 1) ^ 1, ctl, a.status, a.wait_limit_ns);
+        const int st = (it + x) % C::kStages, u = (it + x) / C::kStages;
+        ok = ok && warp_wait(BAR(kBFull + st), u & 1, ctl, a.status, a.wait_limit_ns);
         if (!ok) break;
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          lse_s[slot * 128 + 32 * y + lane] =
+          lse_s[st * 128 + 32 * y + lane] =
               l[x][y] == -INFINITY ? -INFINITY : l[x][y] * -1.4426950408889634f;
-        if (lane == 0) desc[slot] = d[x];
-        mbar_arrive(BAR(kBRF + slot));
+        if (lane == 0) desc[st] = d[x];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(kBDone + st));
       }
     }
   } else {
@@ -417,113 +390,84 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
     const int2* desc = reinterpret_cast<const int2*>(smem + C::kDOff);
     float* xch = reinterpret_cast<float*>(smem + C::kXOff);
     const float sc = a.scale_log2;
-    if (wg == 0 && n_iter > 0)  // every S buffer is free at first
-      for (int k = 0; k < C::kStages; ++k) mbar_arrive(BAR(kBFull + k));
-    uint32_t cm[4] = {0u, 0u, 0u, 0u};  // which of the tile's queries see this key
+    if (n_iter > 0)  // every buffer is free at first
+      for (int k = lane; k < C::kStages; k += 32) mbar_arrive(BAR(kBFull + k));
+    uint32_t cm = 0u;  // which of the tile's queries [32 wg, 32 wg + 32) see this key
     bool ok = true, cut_here = false;
-    int part = 0, it = wg;  // this warpgroup's next unit
+    int part = 0, it = 0;
     int64_t start = f.off;  // first unit of the item
-    int it_end = 0;
-    while (it_end < n_iter) {
+    while (it < n_iter) {
       // ------------------------------------------------------------ one part: units of an item
       const int64_t end = start + static_cast<int64_t>(p.n) * ka.G;
-      it_end += p.units;
+      const int it_end = it + p.units;
       const int item = p.item, n_full = p.n_full, nt = p.nt, bg = p.item / a.Tn;
       const int64_t j = static_cast<int64_t>(nt) * 128 + r;
       const bool key_ok = j < a.Sk;
       float total = 0.f;
       int cm_k = -1;
-      for (; it < it_end; it += kGroups) {
-        const int sb = it % C::kStages, slot = it % kRing;
+      for (; it < it_end; ++it) {
+        const int st = it % C::kStages;
         // (a warp whose wait gave up goes on without work, so that the groups still meet)
         if (ok)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBRF + slot), (it / kRing) & 1, ctl, a.status,
-                                                 a.wait_limit_ns));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBDone + st), (it / C::kStages) & 1, ctl,
+                                                 a.status, a.wait_limit_ns));
         if (!ok) continue;
-        const int2 d = desc[slot];
+        tc_fence_after();
+        uint32_t s[32];
+        tmem_ld32(tl + st * 128 + 32 * wg, s);
+        const int2 d = desc[st];
         const bool partial = d.y >= n_full;
         if (partial && cm_k != d.y) {
           cm_k = d.y;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int64_t q0 = static_cast<int64_t>(d.x) * 128 + 32 * c;
-            uint32_t x = key_ok ? 0xFFFFFFFFu : 0u;
-            if (a.causal) {  // i >= j
-              const int64_t lo = j - q0;
-              x &= lo <= 0 ? 0xFFFFFFFFu : (lo >= 32 ? 0u : (0xFFFFFFFFu << lo));
-            }
-            if (a.mode == SA_MODE_BLOCK && a.bs == 64 && key_ok) {
-              const int64_t mb = q0 / 64;
-              if (!(mb < a.Mb &&
-                    __ldg(a.mask + (static_cast<int64_t>(bg) * a.Mb + mb) * a.Nb + j / 64) != 0))
-                x = 0u;
-            } else if (a.mode == SA_MODE_INDEX) {
-              // lane L loads the presence word of query q0 + L over this warp's 32 keys; the
-              // transpose leaves in lane L the word of key L over the 32 queries
-              const int64_t i = q0 + lane;
-              const int w = nt * 4 + quarter;
-              const uint32_t bits =
-                  (i < a.Sq && w < a.W)
-                      ? __ldg(a.bitmap + (static_cast<int64_t>(bg) * a.Sq + i) * a.W + w)
-                      : 0u;
-              x &= warp_transpose32(bits, lane);
-            }
-            cm[c] = x;
+          const int64_t q0 = static_cast<int64_t>(d.x) * 128 + 32 * wg;
+          cm = key_ok ? 0xFFFFFFFFu : 0u;
+          if (a.causal) {  // i >= j
+            const int64_t lo = j - q0;
+            cm &= lo <= 0 ? 0xFFFFFFFFu : (lo >= 32 ? 0u : (0xFFFFFFFFu << lo));
+          }
+          if (a.mode == SA_MODE_BLOCK && a.bs == 64 && key_ok) {
+            const int64_t mb = q0 / 64;
+            if (!(mb < a.Mb &&
+                  __ldg(a.mask + (static_cast<int64_t>(bg) * a.Mb + mb) * a.Nb + j / 64) != 0))
+              cm = 0u;
+          } else if (a.mode == SA_MODE_INDEX) {
+            // lane L loads the presence word of query q0 + L over this warp's 32 keys; the
+            // transpose leaves in lane L the word of key L over the 32 queries
+            const int64_t i = q0 + lane;
+            const int w = nt * 4 + quarter;
+            const uint32_t bits =
+                (i < a.Sq && w < a.W)
+                    ? __ldg(a.bitmap + (static_cast<int64_t>(bg) * a.Sq + i) * a.W + w)
+                    : 0u;
+            cm &= warp_transpose32(bits, lane);
           }
         }
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBDone + sb), (it / C::kStages) & 1, ctl,
-                                               a.status, a.wait_limit_ns));
-        if (!ok) continue;
-        tc_fence_after();
-        const ulonglong2* ls2 = reinterpret_cast<const ulonglong2*>(lse_s + slot * 128);
+        const ulonglong2* ls2 = reinterpret_cast<const ulonglong2*>(lse_s + st * 128 + 32 * wg);
         uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of sums
+        tmem_wait_ld();
         auto sweep = [&](auto masked) {
           constexpr bool kMasked = decltype(masked)::value;
-          uint32_t buf[2][16];
-          tmem_ld16(tl + sb * 128, buf[0]);
-  #pragma unroll
-          for (int c = 0; c < 8; ++c) {  // 16 columns; the next ones are on their way meanwhile
-            tmem_wait_ld();
-            if (c < 7) tmem_ld16(tl + sb * 128 + 16 * (c + 1), buf[(c + 1) & 1]);
-            else {  // every column is read: the buffer is free
-              tc_fence_before();
-              mbar_arrive(BAR(kBFull + sb));
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const ulonglong2 l = ls2[e >> 1];
+            const uint64_t t2 = fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                     pack2(sc, sc), (e & 1) ? l.y : l.x);
+            const float2 t = unpack2(t2);
+            float p0 = ex2(t.x), p1 = ex2(t.y);
+            if constexpr (kMasked) {
+              p0 = (cm >> (2 * e)) & 1u ? p0 : 0.f;
+              p1 = (cm >> (2 * e + 1)) & 1u ? p1 : 0.f;
             }
-            const uint32_t* s = buf[c & 1];
-  #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const ulonglong2 l = ls2[4 * c + (e >> 1)];
-              const uint64_t t2 = fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
-                                       pack2(sc, sc), (e & 1) ? l.y : l.x);
-              // kPoly of every eight pairs go through the fused multiply-add pipe, the others
-              // through the special-function unit
-              const bool poly = e * kPoly / 8 != (e + 1) * kPoly / 8;
-              const uint32_t bits = cm[c >> 1] >> (16 * (c & 1) + 2 * e);
-              if (poly) {
-                uint64_t p2, s2;
-                exp2_poly(t2, p2, s2);
-                if constexpr (!kMasked) {
-                  ps[e & 3] = fma2(p2, s2, ps[e & 3]);
-                } else {
-                  const float2 pv = unpack2(p2), sv = unpack2(s2);
-                  ps[e & 3] = add2(ps[e & 3], pack2((bits & 1u) ? pv.x * sv.x : 0.f,
-                                                    (bits & 2u) ? pv.y * sv.y : 0.f));
-                }
-              } else {
-                const float2 t = unpack2(t2);
-                float p0 = ex2(t.x), p1 = ex2(t.y);
-                if constexpr (kMasked) {
-                  p0 = (bits & 1u) ? p0 : 0.f;
-                  p1 = (bits & 2u) ? p1 : 0.f;
-                }
-                ps[e & 3] = add2(ps[e & 3], pack2(p0, p1));
-              }
-            }
+            ps[e & 3] = add2(ps[e & 3], pack2(p0, p1));
           }
         };
         if (partial) sweep(std::true_type{});
         else sweep(std::false_type{});
-        mbar_arrive(BAR(kBRE + slot));
+        // S and lse are read.  One arrival for the warp: arrivals of 32 lanes on one barrier are
+        // taken one after another, and 512 of them a unit cost more than its exponentials.
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(kBFull + st));
         const float2 sum = unpack2(add2(add2(ps[0], ps[1]), add2(ps[2], ps[3])));
         total += sum.x + sum.y;
       }
@@ -551,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<DQK>::kThreads, 1)
       }
       start = end;
       ++part;
-      if (it_end < n_iter) p.next(ka, n_iter - it_end);
+      if (it < n_iter) p.next(ka, n_iter - it);
     }
     if (n_iter > 0 && wg == 0 && r == 0 && !cut_here) ka.fix[cta] = make_int2(-1, 0);
   }
@@ -622,7 +566,7 @@ static int launch(const Args& a, const CUtensorMap& mq, const CUtensorMap& mk, c
                       "key weights smem attribute");
   });
   if (rc) return rc;
-  key_weights_kernel<DQK><<<a.C, C::kThreads, C::kSmem, st>>>(mq, mk, a);
+  key_weights_kernel<DQK><<<a.C, kThreads, C::kSmem, st>>>(mq, mk, a);
   return check_launch("key weights kernel launch");
 }
 
