@@ -19,7 +19,7 @@ template <int DQK, int DV>
 struct Cfg {
   static constexpr int kN = DQK <= 128 ? 128 : 64;  // keys of a tile
   static constexpr int kQStages = DQK == 256 ? 1 : 2;
-  static constexpr int kKStages = DQK == 64 ? 5 : 3;
+  static constexpr int kKStages = DQK == 64 ? 5 : 2;  // (a third one measured no faster)
   static constexpr int kVStages = DQK == 64 ? 5 : DQK == 192 ? 3 : 2;
   static constexpr int kQPanel = 128 * 128;  // 64 columns x 128 rows
   static constexpr int kKPanel = kN * 128;   // 64 columns x kN rows (V too)
@@ -31,8 +31,12 @@ struct Cfg {
   // what the two warps of a quarter exchange, [2][128]: a tile's row maxima, a part's row sums
   // (a barrier of the pair lies between one use's reads and the next one's writes)
   static constexpr int kXOff = kVOff + kVStages * kVBytes;
-  static constexpr int kFindOff = kXOff + 1024;
-  static constexpr int kBarOff = kFindOff + 66 * 8;
+  static constexpr int kMOff = kXOff + 1024;  // a part's row maxima, [128]
+  // where the four copies of a row meet at a part's end: [2 column halves][4][32 rows][32 columns]
+  static constexpr int kMergeOff = kMOff + 512;
+  // (what find_range needs lies there too: every warp is past it when the first part ends)
+  static constexpr int kFindOff = kMergeOff;
+  static constexpr int kBarOff = kMergeOff + 32 * 1024;
   static constexpr int kSmem = kBarOff + 256 + 1024;
   static constexpr int kThreads = 352;
   static constexpr uint32_t kOCol = 256;  // S / P buffers at columns 0 and 128
@@ -74,6 +78,8 @@ __global__ void __launch_bounds__(352, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  wait_previous_kernel();
+  allow_next_kernel();
   const Found f = find_range<C::kThreads>(
       a, cta, reinterpret_cast<int64_t*>(smem + C::kFindOff));  // (ends with a barrier)
   tc_fence_after();
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(352, 1)
     float* xch = reinterpret_cast<float*>(smem + C::kXOff);
     const int r = quarter * 32 + lane;
     float m_run = -INFINITY, l_run = 0.f;
-    bool first = true;
+    bool first = true, ok = true;
     auto both = [&](bool v) { return named_bar_and(pair_bar, 64, v); };
     // One tile: S columns [c0, c0 + NC) of this thread's row -> P.  kRep: the row's copy in
     // this quarter takes the quarter's kN / 4 columns, the others' P is zero.
@@ -317,55 +323,110 @@ __global__ void __launch_bounds__(352, 1)
       const bool rep = (w.prefix ? a.rep_p : a.rep_c) > 1;
       const int rows = w.prefix ? a.rows_p : a.rows_c;
       const bool active = (rep ? lane : r) < rows;
-      const bool done = rep ? tile(std::integral_constant<int, kN / 8>{}, true, it, active)
-                            : tile(std::integral_constant<int, kN / 2>{}, false, it, active);
-      if (!done) break;
+      // (after a wait that gave up the loop goes on without work, so that the warps still meet
+      // at the barriers of a part's end)
+      if (ok)
+        ok = rep ? tile(std::integral_constant<int, kN / 8>{}, true, it, active)
+                 : tile(std::integral_constant<int, kN / 2>{}, false, it, active);
       const int lim = static_cast<int>(min64(kN, w.keys - w.tile * kN));
-      if (!w.prefix && lim < kN) {
+      if (ok && !w.prefix && lim < kN) {
         // the V rows behind the sequence hold anything, and 0 x NaN is NaN: clear them
         const int vs = it % C::kVStages, vu = it / C::kVStages;
-        if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBVF + vs), vu & 1, ctl, a.status,
-                                                    a.wait_limit_ns))))
-          break;
-        uint8_t* vt = smem + C::kVOff + vs * C::kVBytes;
-        const int n = (kN - lim) * (DV / 8);
-        for (int e = threadIdx.x - 64; e < n; e += 256) {
-          const int row = lim + e / (DV / 8), ch = e % (DV / 8);
-          *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kKPanel + row * 128 + (ch & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+        ok = both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBVF + vs), vu & 1, ctl, a.status,
+                                                    a.wait_limit_ns)));
+        if (ok) {
+          uint8_t* vt = smem + C::kVOff + vs * C::kVBytes;
+          const int n = (kN - lim) * (DV / 8);
+          for (int e = threadIdx.x - 64; e < n; e += 256) {
+            const int row = lim + e / (DV / 8), ch = e % (DV / 8);
+            *reinterpret_cast<uint4*>(vt + (ch >> 3) * C::kKPanel + row * 128 + (ch & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(BAR(kBPF + (it & 1)));
+      if (ok) {
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(BAR(kBPF + (it & 1)));
+      }
       const Walk at = w;
       first = it + 1 == n_iter || w.next(a);
       if (first) {
         // ------------------------------------------------------------ a part ends
-        if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), it & 1, ctl, a.status,
-                                                    a.wait_limit_ns))))
-          break;
+        if (ok)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), it & 1, ctl, a.status, a.wait_limit_ns));
+        ok = named_bar_and(8, 256, ok);
+        if (!ok) continue;
         tc_fence_after();
-        xch[hc * 128 + r] = l_run;
-        named_bar_sync(pair_bar, 64);
-        const float l = xch[r] + xch[128 + r];
         const int64_t slot = at.seg + cta;
-        const int64_t row = rep ? (slot * 4 + quarter) * rows + lane : slot * rows + r;
-        float* po = (at.prefix ? a.po_p : a.po_c) + row * DV;
+        float2* mls = (at.prefix ? a.ml_p : a.ml_c) + slot * rows;
+        float* po = (at.prefix ? a.po_p : a.po_c) + slot * rows * DV;
+        xch[hc * 128 + r] = l_run;
+        if (!rep) {
+          named_bar_sync(pair_bar, 64);
+          if (active && hc == 0) mls[r] = make_float2(m_run, xch[r] + xch[128 + r]);
 #pragma unroll 1
-        for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
-          uint32_t ov[32];
-          tmem_ld32(tl + C::kOCol + c, ov);
-          tmem_wait_ld();
-          if (active) {
+          for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tl + C::kOCol + c, ov);
+            tmem_wait_ld();
+            if (active) {
+              uint4* dst = reinterpret_cast<uint4*>(po + static_cast<int64_t>(r) * DV + c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(po + c + 4 * e) =
-                  make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+            }
+          }
+        } else {
+          // the four copies of a row (each over its own keys) become one result
+          float* xm = reinterpret_cast<float*>(smem + C::kMOff);
+          if (hc == 0) xm[r] = m_run;
+          named_bar_sync(5, 256);
+          float mm = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mm = fmaxf(mm, xm[32 * q + lane]);
+          const float me = mm == -INFINITY ? 0.f : mm;
+          const float f = ex2(m_run - me);
+          if (active && quarter == 0 && hc == 0) {
+            float l = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              l += (xch[32 * q + lane] + xch[128 + 32 * q + lane]) * ex2(xm[32 * q + lane] - me);
+            mls[lane] = make_float2(mm, l);
+          }
+          uint8_t* stage = smem + C::kMergeOff + hc * 16384;
+#pragma unroll 1
+          for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tl + C::kOCol + c, ov);
+            tmem_wait_ld();
+            if (active) {
+              float4* dst = reinterpret_cast<float4*>(stage + (quarter * rows + lane) * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e ^ (lane & 7)] =
+                    make_float4(__uint_as_float(ov[4 * e]) * f, __uint_as_float(ov[4 * e + 1]) * f,
+                                __uint_as_float(ov[4 * e + 2]) * f, __uint_as_float(ov[4 * e + 3]) * f);
+            }
+            named_bar_sync(6 + hc, 128);
+            for (int e = quarter * 32 + lane; e < rows * 8; e += 128) {
+              const int row = e >> 3, ch = e & 7;
+              float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 x = *reinterpret_cast<const float4*>(stage + (q * rows + row) * 128 +
+                                                                  ((ch ^ (row & 7)) << 4));
+                o.x += x.x;
+                o.y += x.y;
+                o.z += x.z;
+                o.w += x.w;
+              }
+              *reinterpret_cast<float4*>(po + static_cast<int64_t>(row) * DV + c + 4 * ch) = o;
+            }
+            named_bar_sync(6 + hc, 128);  // the stage may be written again
           }
         }
-        if (active && hc == 0) (at.prefix ? a.ml_p : a.ml_c)[row] = make_float2(m_run, l);
         tc_fence_before();
         m_run = -INFINITY;
         l_run = 0.f;
@@ -405,7 +466,8 @@ __global__ void __launch_bounds__(352, 1)
 }
 
 // ------------------------------------------------------------------------------------
-// join: one block per (sequence, query head)
+// join: one block per (sequence, query head).  Every warp finds the parts' common maximum and
+// sum (one part per lane), then takes every fourth part's output, four loads in flight.
 // ------------------------------------------------------------------------------------
 constexpr int kJoin = 128;
 
@@ -413,7 +475,7 @@ template <int DV>
 __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   constexpr int kW = kJoin / 32, kD = DV / 32;
   __shared__ int64_t shs[2][kW];
-  __shared__ float sh_o[kW][DV], sh_m[kW], sh_l[kW];
+  __shared__ float sh_o[kW][DV];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / a.HQ, h = blockIdx.x - b * a.HQ;
   const int hk = h / a.G, g = h - hk * a.G;
@@ -442,76 +504,82 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   const int64_t np = a.Tp * a.Rt * a.HK, U = np + total * a.HK;
   const int C = busy_ctas(a, U);
   const int64_t tb = tiles_of(a, clamped_len(a, b));
-  // parts of the prefix (of this row's tile) and of the own cache
+  // parts of the prefix (of this row's tile) and of the own cache: rows of ml / po, `step` apart
   int n_p = 0, n_c = 0;
-  int64_t slot_p = 0, slot_c = 0;
-  int row_p = 0;
+  int64_t at_p = 0, at_c = 0;
   if (np > 0) {
     const int rt = b / a.nb;
     const int64_t seg = static_cast<int64_t>(hk) * a.Rt + rt;
     const int c0 = cta_of(seg * a.Tp, U, C), c1 = cta_of(seg * a.Tp + a.Tp - 1, U, C);
     n_p = c1 - c0 + 1;
-    slot_p = seg + c0;
-    row_p = g * a.nb + (b - rt * a.nb);
+    at_p = (seg + c0) * a.rows_p + g * a.nb + (b - rt * a.nb);
   }
   if (tb > 0) {
     const int64_t u = np + before * a.HK + hk * tb;
     const int c0 = cta_of(u, U, C), c1 = cta_of(u + tb - 1, U, C);
     n_c = c1 - c0 + 1;
-    slot_c = static_cast<int64_t>(b) * a.HK + hk + c0;
+    at_c = (static_cast<int64_t>(b) * a.HK + hk + c0) * a.rows_c + g;
   }
-  const int nr_p = n_p * a.rep_p, n = nr_p + n_c * a.rep_c;
-  float m = -INFINITY, l = 0.f, acc[kD];
+  const int n = n_p + n_c;
+  auto ml_of = [&](int i) {
+    return i < n_p ? a.ml_p + at_p + static_cast<int64_t>(i) * a.rows_p
+                   : a.ml_c + at_c + static_cast<int64_t>(i - n_p) * a.rows_c;
+  };
+  auto po_of = [&](int i) {
+    return i < n_p ? a.po_p + (at_p + static_cast<int64_t>(i) * a.rows_p) * DV
+                   : a.po_c + (at_c + static_cast<int64_t>(i - n_p) * a.rows_c) * DV;
+  };
+  wait_previous_kernel();
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, ml_of(i)->x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  const float me = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[kD];
 #pragma unroll
   for (int e = 0; e < kD; ++e) acc[e] = 0.f;
-  for (int i = warp; i < n; i += kW) {
-    const float2* ml;
-    const float* po;
-    if (i < nr_p) {
-      const int64_t at = (slot_p * a.rep_p + i) * a.rows_p + row_p;
-      ml = a.ml_p + at;
-      po = a.po_p + at * DV;
-    } else {
-      const int64_t at = (slot_c * a.rep_c + (i - nr_p)) * a.rows_c + g;
-      ml = a.ml_c + at;
-      po = a.po_c + at * DV;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float f = 0.f;  // of part i0 + lane (0: a part without keys)
+    if (i0 + lane < n) {
+      const float2 v = *ml_of(i0 + lane);
+      if (v.y != 0.f) {
+        f = ex2(v.x - me);
+        l += v.y * f;
+      }
     }
-    const float2 v = *ml;
-    float x[kD];
+    const int left = min(32, n - i0);
+    for (int x = warp; x < left; x += 4 * kW) {
+      float v[4][kD], fx[4];
 #pragma unroll
-    for (int e = 0; e < kD; ++e) x[e] = po[e * 32 + lane];
-    const float mn = fmaxf(m, v.x);
-    if (v.y == 0.f) continue;  // a part without keys
-    const float f0 = ex2(m - mn), f1 = ex2(v.x - mn);
-    m = mn;
-    l = l * f0 + v.y * f1;
+      for (int y = 0; y < 4; ++y) {
+        const int i = x + y * kW;
+        fx[y] = __shfl_sync(0xFFFFFFFFu, f, i & 31);
+        if (i >= left) fx[y] = 0.f;
+        if (fx[y] != 0.f) {
+          const float* po = po_of(i0 + i);
 #pragma unroll
-    for (int e = 0; e < kD; ++e) acc[e] = acc[e] * f0 + x[e] * f1;
+          for (int e = 0; e < kD; ++e) v[y][e] = po[e * 32 + lane];
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (fx[y] != 0.f) {
+#pragma unroll
+          for (int e = 0; e < kD; ++e) acc[e] = fmaf(v[y][e], fx[y], acc[e]);
+        }
+    }
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
 #pragma unroll
   for (int e = 0; e < kD; ++e) sh_o[warp][e * 32 + lane] = acc[e];
-  if (lane == 0) {
-    sh_m[warp] = m;
-    sh_l[warp] = l;
-  }
   __syncthreads();
-  m = -INFINITY;
-#pragma unroll
-  for (int x = 0; x < kW; ++x) m = fmaxf(m, sh_m[x]);
-  const float me = m == -INFINITY ? 0.f : m;
-  l = 0.f;
-  float f[kW];
-#pragma unroll
-  for (int x = 0; x < kW; ++x) {
-    f[x] = ex2(sh_m[x] - me);
-    l += sh_l[x] * f[x];
-  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t row = static_cast<int64_t>(b) * a.HQ + h;
   for (int d = tid; d < DV; d += kJoin) {
     float o = 0.f;
 #pragma unroll
-    for (int x = 0; x < kW; ++x) o += sh_o[x][d] * f[x];
+    for (int x = 0; x < kW; ++x) o += sh_o[x][d];
     a.o[row * DV + d] = __float2bfloat16(o * inv);
   }
   if (tid == 0) a.lse[row] = l == 0.f ? -INFINITY : (me + __log2f(l)) * 0.69314718055994531f;
@@ -523,9 +591,10 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
 __global__ void __launch_bounds__(256) cache_weights_kernel(const Args a) {
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int hk = blockIdx.y, b = blockIdx.z;
-  if (j >= a.S) return;
+  if (j >= a.S) return;  // (a block that leaves early has nothing to wait for)
   const int64_t at = (static_cast<int64_t>(b) * a.HK + hk) * a.S + j;
   const bool live = j < clamped_len(a, b);
+  wait_previous_kernel();
   if (!live && a.w_in == a.w_out) return;
   float w = a.w_in ? a.w_in[at] : 0.f;
   if (live) {
@@ -564,14 +633,14 @@ static int launch(const Args& a, cudaStream_t st) {
                   !make_map(&m.kp, a.kp, DQK, a.P, a.HK, 1, C::kN) ||
                   !make_map(&m.vp, a.vp, DV, a.P, a.HK, 1, C::kN)))
     return SA_ERR_CUDA;
-  cache_part_kernel<DQK, DV><<<a.C, C::kThreads, C::kSmem, st>>>(m, a);
-  rc = check_launch("cache attention kernel launch");
+  rc = launch_early(cache_part_kernel<DQK, DV>, dim3(a.C), dim3(C::kThreads), C::kSmem, st,
+                    "cache attention kernel launch", m, a);
   if (rc) return rc;
-  cache_join_kernel<DV><<<static_cast<unsigned>(a.B * a.HQ), kJoin, 0, st>>>(a);
-  rc = check_launch("cache join kernel launch");
+  rc = launch_early(cache_join_kernel<DV>, dim3(static_cast<unsigned>(a.B * a.HQ)), dim3(kJoin), 0,
+                    st, "cache join kernel launch", a);
   if (rc || !a.w_out) return rc;
-  cache_weights_kernel<<<dim3(static_cast<unsigned>((a.S + 255) / 256), a.HK, a.B), 256, 0, st>>>(a);
-  return check_launch("cache weights kernel launch");
+  return launch_early(cache_weights_kernel, dim3(static_cast<unsigned>((a.S + 255) / 256), a.HK, a.B),
+                      dim3(256), 0, st, "cache weights kernel launch", a);
 }
 
 static size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -594,10 +663,10 @@ static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
   a->Tp = (p->P + a->kn - 1) / a->kn;
   a->rows_p = a->nb * a->G;
   a->rows_c = a->G;
-  a->rep_p = a->rows_p <= 32 ? 4 : 1;
+  a->rep_p = a->rows_p <= 32 ? 4 : 1;  // (few rows: a copy in each TMEM lane quarter)
   a->rep_c = a->rows_c <= 32 ? 4 : 1;
-  const size_t parts_p = p->P ? (static_cast<size_t>(a->HK) * a->Rt + kMaxCtas) * a->rep_p * a->rows_p : 0;
-  const size_t parts_c = (static_cast<size_t>(p->B) * p->HK + kMaxCtas) * a->rep_c * a->rows_c;
+  const size_t parts_p = p->P ? (static_cast<size_t>(a->HK) * a->Rt + kMaxCtas) * a->rows_p : 0;
+  const size_t parts_c = (static_cast<size_t>(p->B) * p->HK + kMaxCtas) * a->rows_c;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* q = ws ? ws + off : nullptr;

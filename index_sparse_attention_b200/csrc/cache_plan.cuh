@@ -38,8 +38,8 @@ struct Args {
   int nb;            // sequences of one prefix row tile: rows g * nb + (b - nb * tile)
   int Rt;            // prefix row tiles per KV head
   int64_t Tp;        // prefix key tiles
-  int rep_p, rep_c;  // partial results per row of a part
-  int rows_p, rows_c;  // rows of one partial
+  int rep_p, rep_c;    // copies of a part's rows in the TMEM lane quarters (4 or 1)
+  int rows_p, rows_c;  // rows of a part
   int C;             // CTAs
   float scale_log2;
   int32_t* status;

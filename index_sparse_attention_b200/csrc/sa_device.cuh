@@ -405,6 +405,18 @@ __device__ __forceinline__ void tmem_wait_st() {
 #undef SA_W8
 
 // ---------------------------------------------------------------------------------
+// Programmatic dependent launch (launch_early in sa_kernels.h): a kernel so launched may start
+// while the one before it in the stream still runs, and reads nothing that one writes (and
+// writes nothing that one reads) before wait_previous_kernel().
+// ---------------------------------------------------------------------------------
+__device__ __forceinline__ void wait_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void allow_next_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------------
 // UMMA descriptors
 // ---------------------------------------------------------------------------------
 // Shared-memory matrix descriptor for a 128-byte-swizzled operand (sm_100 format:

@@ -67,6 +67,25 @@ inline void record_event(int k, cudaStream_t st) {
 int cuda_error(cudaError_t e, const char* what);
 inline int check_launch(const char* what) { return cuda_error(cudaGetLastError(), what); }
 
+// Launches `kern` so that it may start before the kernel ahead of it in the stream has ended
+// (it waits for that kernel itself, wait_previous_kernel()): its launch and set-up overlap
+// that kernel's end.
+template <class... P, class... A>
+inline int launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                        const char* what, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_error(cudaLaunchKernelEx(&cfg, kern, args...), what);
+}
+
 // Runs `set` (a cudaFuncSetAttribute call and the like) once per device: a flag bit per
 // device index (< 64), set only when `set` returns SA_OK, so a failure is retried on
 // the next call; thread-safe.  Device = the current device.
