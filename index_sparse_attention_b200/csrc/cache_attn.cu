@@ -73,6 +73,16 @@ __global__ void __launch_bounds__(352, 1)
     ctl->abort = 0;
     fence_mbar_init();
   }
+  if (warp == 10 && lane == 0) {
+    prefetch_tensormap(&maps.qc);
+    prefetch_tensormap(&maps.kc);
+    prefetch_tensormap(&maps.vc);
+    if (a.P > 0) {
+      prefetch_tensormap(&maps.qp);
+      prefetch_tensormap(&maps.kp);
+      prefetch_tensormap(&maps.vp);
+    }
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -193,7 +203,10 @@ __global__ void __launch_bounds__(352, 1)
     };
     bool ok = n_iter > 0 && issue_s(0);
     for (int it = 0; ok && it < n_iter; ++it) {
-      if (it + 1 < n_iter && !issue_s(it + 1)) break;
+      // the next S before this P V, so that the softmax has its next tile; at a part's end
+      // after it, because the epilogue waits for O and then takes longer than S
+      const bool last = first_s;
+      if (!last && it + 1 < n_iter && !issue_s(it + 1)) break;
       const int vs = it % C::kVStages, vu = it / C::kVStages;
       if (!warp_wait(BAR(kBPF + (it & 1)), (it >> 1) & 1, ctl, a.status, a.wait_limit_ns)) break;
       if (!warp_wait(BAR(kBVF + vs), vu & 1, ctl, a.status, a.wait_limit_ns)) break;
@@ -209,6 +222,7 @@ __global__ void __launch_bounds__(352, 1)
       }
       __syncwarp();
       if (it + 1 < n_iter) first_o = wo.next(a);
+      if (last && it + 1 < n_iter && !issue_s(it + 1)) break;
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -395,36 +409,42 @@ __global__ void __launch_bounds__(352, 1)
               l += (xch[32 * q + lane] + xch[128 + 32 * q + lane]) * ex2(xm[32 * q + lane] - me);
             mls[lane] = make_float2(mm, l);
           }
-          uint8_t* stage = smem + C::kMergeOff + hc * 16384;
+          // up to eight rows: all columns of this half at once, else 32 at a time
+          float* stage = reinterpret_cast<float*>(smem + C::kMergeOff + hc * 16384);
+          const int cp = rows <= 8 ? DV / 2 : 32;
 #pragma unroll 1
-          for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
-            uint32_t ov[32];
-            tmem_ld32(tl + C::kOCol + c, ov);
-            tmem_wait_ld();
-            if (active) {
-              float4* dst = reinterpret_cast<float4*>(stage + (quarter * rows + lane) * 128);
+          for (int c0 = hc * (DV / 2); c0 < (hc + 1) * (DV / 2); c0 += cp) {
+            if (c0 != hc * (DV / 2)) named_bar_sync(6 + hc, 128);  // the last pass is read
+#pragma unroll 1
+            for (int c = 0; c < cp; c += 32) {
+              uint32_t ov[32];
+              tmem_ld32(tl + C::kOCol + c0 + c, ov);
+              tmem_wait_ld();
+              if (active) {
+                float4* dst = reinterpret_cast<float4*>(stage + (quarter * rows + lane) * cp + c);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e ^ (lane & 7)] =
-                    make_float4(__uint_as_float(ov[4 * e]) * f, __uint_as_float(ov[4 * e + 1]) * f,
-                                __uint_as_float(ov[4 * e + 2]) * f, __uint_as_float(ov[4 * e + 3]) * f);
+                for (int e = 0; e < 8; ++e)
+                  dst[e ^ (lane & 7)] = make_float4(
+                      __uint_as_float(ov[4 * e]) * f, __uint_as_float(ov[4 * e + 1]) * f,
+                      __uint_as_float(ov[4 * e + 2]) * f, __uint_as_float(ov[4 * e + 3]) * f);
+              }
             }
             named_bar_sync(6 + hc, 128);
-            for (int e = quarter * 32 + lane; e < rows * 8; e += 128) {
-              const int row = e >> 3, ch = e & 7;
+            const int per = cp / 4;  // float4 of a row
+            for (int e = quarter * 32 + lane; e < rows * per; e += 128) {
+              const int row = e / per, ch = e - row * per;
               float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const float4 x = *reinterpret_cast<const float4*>(stage + (q * rows + row) * 128 +
-                                                                  ((ch ^ (row & 7)) << 4));
+                const float4 x = *reinterpret_cast<const float4*>(
+                    stage + (q * rows + row) * cp + 4 * (ch ^ (row & 7)));
                 o.x += x.x;
                 o.y += x.y;
                 o.z += x.z;
                 o.w += x.w;
               }
-              *reinterpret_cast<float4*>(po + static_cast<int64_t>(row) * DV + c + 4 * ch) = o;
+              *reinterpret_cast<float4*>(po + static_cast<int64_t>(row) * DV + c0 + 4 * ch) = o;
             }
-            named_bar_sync(6 + hc, 128);  // the stage may be written again
           }
         }
         tc_fence_before();
@@ -466,22 +486,28 @@ __global__ void __launch_bounds__(352, 1)
 }
 
 // ------------------------------------------------------------------------------------
-// join: one block per (sequence, query head).  Every warp finds the parts' common maximum and
-// sum (one part per lane), then takes every fourth part's output, four loads in flight.
+// join: kW warps per (sequence, query head) row, 4 / kW rows per block.  Every warp finds the
+// parts' common maximum and sum (one part per lane), then takes every kW-th part's output, four
+// loads in flight.  Few rows have many parts (up to one per CTA) and take four warps each; from
+// kJoinRows rows on the blocks are many and the parts few, and a warp does a row (8192 rows of
+// two or three parts: 36 us with four warps, 17 with one).
 // ------------------------------------------------------------------------------------
 constexpr int kJoin = 128;
+constexpr int kJoinRows = 2048;
 
-template <int DV>
+template <int DV, int kW>
 __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
-  constexpr int kW = kJoin / 32, kD = DV / 32;
-  __shared__ int64_t shs[2][kW];
-  __shared__ float sh_o[kW][DV];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / a.HQ, h = blockIdx.x - b * a.HQ;
+  constexpr int kD = DV / 32, kRows = 4 / kW;
+  __shared__ float sh_o[kW > 1 ? kW : 1][DV];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = kW > 1 ? tid >> 5 : 0;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kW > 1 ? 0 : tid >> 5);
+  if (row >= static_cast<int64_t>(a.B) * a.HQ) return;  // (kW == 1 only: a whole warp)
+  const int b = static_cast<int>(row / a.HQ), h = static_cast<int>(row - static_cast<int64_t>(b) * a.HQ);
   const int hk = h / a.G, g = h - hk * a.G;
-  // tiles before this sequence and in all
+  // tiles before this sequence and in all (every warp for itself)
   int64_t before = 0, total = 0;
-  for (int x = tid; x < a.B; x += kJoin) {
+  for (int x = lane; x < a.B; x += 32) {
     const int64_t t = tiles_of(a, clamped_len(a, x));
     total += t;
     if (x < b) before += t;
@@ -490,16 +516,6 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   for (int d = 16; d; d >>= 1) {
     before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
     total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
-  }
-  if (lane == 0) {
-    shs[0][warp] = before;
-    shs[1][warp] = total;
-  }
-  __syncthreads();
-  before = total = 0;
-  for (int x = 0; x < kW; ++x) {
-    before += shs[0][x];
-    total += shs[1][x];
   }
   const int64_t np = a.Tp * a.Rt * a.HK, U = np + total * a.HK;
   const int C = busy_ctas(a, U);
@@ -571,18 +587,23 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-#pragma unroll
-  for (int e = 0; e < kD; ++e) sh_o[warp][e * 32 + lane] = acc[e];
-  __syncthreads();
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t row = static_cast<int64_t>(b) * a.HQ + h;
-  for (int d = tid; d < DV; d += kJoin) {
-    float o = 0.f;
+  if constexpr (kW > 1) {
 #pragma unroll
-    for (int x = 0; x < kW; ++x) o += sh_o[x][d];
-    a.o[row * DV + d] = __float2bfloat16(o * inv);
+    for (int e = 0; e < kD; ++e) sh_o[warp][e * 32 + lane] = acc[e];
+    __syncthreads();
+    for (int d = tid; d < DV; d += kJoin) {
+      float o = 0.f;
+#pragma unroll
+      for (int x = 0; x < kW; ++x) o += sh_o[x][d];
+      a.o[row * DV + d] = __float2bfloat16(o * inv);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kD; ++e) a.o[row * DV + e * 32 + lane] = __float2bfloat16(acc[e] * inv);
   }
-  if (tid == 0) a.lse[row] = l == 0.f ? -INFINITY : (me + __log2f(l)) * 0.69314718055994531f;
+  if (lane == 0 && warp == 0)
+    a.lse[row] = l == 0.f ? -INFINITY : (me + __log2f(l)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------------------------
@@ -636,8 +657,12 @@ static int launch(const Args& a, cudaStream_t st) {
   rc = launch_early(cache_part_kernel<DQK, DV>, dim3(a.C), dim3(C::kThreads), C::kSmem, st,
                     "cache attention kernel launch", m, a);
   if (rc) return rc;
-  rc = launch_early(cache_join_kernel<DV>, dim3(static_cast<unsigned>(a.B * a.HQ)), dim3(kJoin), 0,
-                    st, "cache join kernel launch", a);
+  const int64_t rows = static_cast<int64_t>(a.B) * a.HQ;
+  rc = rows < kJoinRows
+           ? launch_early(cache_join_kernel<DV, 4>, dim3(static_cast<unsigned>(rows)), dim3(kJoin), 0,
+                          st, "cache join kernel launch", a)
+           : launch_early(cache_join_kernel<DV, 1>, dim3(static_cast<unsigned>((rows + 3) / 4)),
+                          dim3(kJoin), 0, st, "cache join kernel launch", a);
   if (rc || !a.w_out) return rc;
   return launch_early(cache_weights_kernel, dim3(static_cast<unsigned>((a.S + 255) / 256), a.HK, a.B),
                       dim3(256), 0, st, "cache weights kernel launch", a);
