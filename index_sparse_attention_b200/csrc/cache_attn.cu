@@ -655,17 +655,17 @@ static int launch(const Args& a, cudaStream_t st) {
                   !make_map(&m.vp, a.vp, DV, a.P, a.HK, 1, C::kN)))
     return SA_ERR_CUDA;
   rc = launch_early(cache_part_kernel<DQK, DV>, dim3(a.C), dim3(C::kThreads), C::kSmem, st,
-                    "cache attention kernel launch", m, a);
+                    "cache attention kernel launch", 1, m, a);
   if (rc) return rc;
   const int64_t rows = static_cast<int64_t>(a.B) * a.HQ;
   rc = rows < kJoinRows
            ? launch_early(cache_join_kernel<DV, 4>, dim3(static_cast<unsigned>(rows)), dim3(kJoin), 0,
-                          st, "cache join kernel launch", a)
+                          st, "cache join kernel launch", 1, a)
            : launch_early(cache_join_kernel<DV, 1>, dim3(static_cast<unsigned>((rows + 3) / 4)),
-                          dim3(kJoin), 0, st, "cache join kernel launch", a);
+                          dim3(kJoin), 0, st, "cache join kernel launch", 1, a);
   if (rc || !a.w_out) return rc;
   return launch_early(cache_weights_kernel, dim3(static_cast<unsigned>((a.S + 255) / 256), a.HK, a.B),
-                      dim3(256), 0, st, "cache weights kernel launch", a);
+                      dim3(256), 0, st, "cache weights kernel launch", 1, a);
 }
 
 static size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

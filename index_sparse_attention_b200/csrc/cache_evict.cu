@@ -3,13 +3,19 @@
 // Per (sequence, KV head) of n > budget keys: the first `sinks`, the last `recent` and the
 // budget - sinks - recent heaviest keys between them stay, in their order.  Two launches:
 // selection (which positions stay) and the copy of the kept rows.
-//   selection  one CTA per (sequence, KV head): radix select of the smallest kept weight in
-//              four digit passes of 8 bits over order-preserving keys (every pass reads the row
-//              again, from L2), then one pass in position order that writes the positions whose
-//              key is above the threshold, and of those equal to it the first ones that are
-//              still needed.
-//   copy       one CTA per eight output rows of a sequence: 16-byte pieces, writes contiguous
-//              over all heads of a row, reads a contiguous piece per (row, head).
+//   selection  a cluster of 1 to 8 CTAs per (sequence, KV head), a slice of the row each, held
+//              in registers as order-preserving keys (4, 8 or 16 per thread; longer slices are
+//              read again in every sweep).  Radix select of the smallest kept weight in three
+//              digit passes (11, 11, 10 bits): each CTA counts its keys in shared memory and adds
+//              up a share of the bins over the cluster (distributed shared memory) for all.  Then every warp counts its stretch of the
+//              row by ballots, one scan over the warps and CTAs gives each its place, and a last
+//              sweep writes the positions in order: keys above the threshold, and of those equal
+//              to it the first ones that are still needed.  The sweeps are bound by their
+//              instructions (with the slice in shared memory and 64-bit positions: 39 us for 32
+//              rows of 65536; with registers xx).
+//   copy       16-byte pieces, four rows per thread in flight, writes contiguous over all heads
+//              of a row.
+// The copy is bound by HBM (each kept row is read and written once).
 #include "sa_device.cuh"
 #include "sa_kernels.h"
 
@@ -18,6 +24,10 @@ namespace evict {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kSlice = 8192;        // keys a CTA takes before the row is spread over more of them
+constexpr int kMaxCluster = 8;
+constexpr int kMaxCtas = 128;       // CTAs that run at once (clusters do not fill every SM)
 
 struct Args {
   const uint4 *k, *v;
@@ -29,6 +39,7 @@ struct Args {
   int B, HK, kp, vp;  // kp, vp: 16-byte pieces of a K / V row of one head
   int64_t S, So;
   int budget, sinks, recent;
+  int cluster;
   int32_t* status;
 };
 
@@ -40,129 +51,244 @@ __device__ __forceinline__ uint32_t weight_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of `v` over the block in thread order; `sum` gets the total.
-__device__ __forceinline__ int block_prefix(int v, int* sh, int& sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+__device__ __forceinline__ int cluster_load(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Inclusive sum over the lanes of a warp.
+__device__ __forceinline__ int warp_scan(int x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int t = __shfl_up_sync(0xFFFFFFFFu, x, d);
     if (lane >= d) x += t;
   }
-  __syncthreads();
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  int t = lane < kWarps ? sh[lane] : 0, y = t;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int z = __shfl_up_sync(0xFFFFFFFFu, y, d);
-    if (lane >= d) y += z;
-  }
-  sum = __shfl_sync(0xFFFFFFFFu, y, 31);
-  return x - v + __shfl_sync(0xFFFFFFFFu, y - t, warp);
+  return x;
 }
 
+// KPT: keys per thread held in registers; 0: read from memory in every sweep.
+template <int KPT>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
-  __shared__ int hist[256];
-  __shared__ int sh[kWarps];
-  __shared__ int pick[2];  // digit, keys above it
-  const int tid = threadIdx.x;
-  const int b = blockIdx.x / a.HK, hk = blockIdx.x - b * a.HK;
+  __shared__ int hist[3][kBins];  // own counts of the three passes
+  __shared__ int all[kBins];      // the cluster's of a pass
+  __shared__ int warp_sum[kWarps], warp_eq[kWarps];
+  __shared__ int pick[2];    // digit, keys above it
+  __shared__ int counts[2];  // this CTA's keys above the threshold and equal to it
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank()), cl = a.cluster;
+  const int64_t row = blockIdx.x / cl;
+  const int b = static_cast<int>(row / a.HK), hk = static_cast<int>(row - static_cast<int64_t>(b) * a.HK);
+  wait_previous_kernel();
+  allow_next_kernel();
   const int raw = __ldg(a.lens + b);
-  const int64_t n = min64(max64(static_cast<int64_t>(raw), 0), a.S);
-  if (tid == 0 && hk == 0) {
+  const int n = static_cast<int>(min64(max64(static_cast<int64_t>(raw), 0), a.S));
+  if (tid == 0 && hk == 0 && rank == 0) {
     if (raw != n) report_status(a.status, kStatusIndex);
-    a.lens_o[b] = static_cast<int32_t>(min64(n, a.budget));
+    a.lens_o[b] = min(n, a.budget);
   }
-  const int64_t row = static_cast<int64_t>(b) * a.HK + hk;
   const float* w = a.w + row * a.S;
   float* wo = a.wo + row * a.So;
   int32_t* keep = a.keep + row * a.budget;
-  const int n_out = static_cast<int>(min64(n, a.budget));
-  for (int64_t i = n_out + tid; i < a.So; i += kThreads) wo[i] = 0.f;
-  for (int i = n_out + tid; i < a.budget; i += kThreads) keep[i] = -1;
-  if (n <= a.budget) {
-    for (int i = tid; i < n_out; i += kThreads) {
+  const int n_out = min(n, a.budget);
+  const int step = cl * kThreads, first = rank * kThreads + tid;
+  for (int64_t i = n_out + first; i < a.So; i += step) wo[i] = 0.f;
+  for (int i = n_out + first; i < a.budget; i += step) keep[i] = -1;
+  if (n <= a.budget) {  // (the same on every CTA of the cluster)
+    for (int i = first; i < n_out; i += step) {
       keep[i] = i;
-      wo[i] = w[i];
+      wo[i] = __ldg(w + i);
     }
     return;
   }
-  const int64_t lo = a.sinks, hi = n - a.recent;  // the candidates
-  int need = a.budget - a.sinks - a.recent;       // of which so many stay (fewer than hi - lo)
+  const int lo = a.sinks, hi = n - a.recent;         // the candidates
+  const int chosen = a.budget - a.sinks - a.recent;  // of which so many stay (fewer than hi - lo)
+  // this warp's stretch [w0, w1) of this CTA's slice of the row, both in whole 32s
+  const int per_cta = ((n + cl - 1) / cl + 31) / 32 * 32;
+  const int s0 = min(n, rank * per_cta), s1 = min(n, s0 + per_cta);
+  const int per_warp = ((s1 - s0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int w0 = min(s1, s0 + warp * per_warp), w1 = min(s1, w0 + per_warp);
+  const int sweeps = KPT > 0 ? KPT : (w1 - w0 + 31) / 32;
+  constexpr int kUnroll = KPT > 0 ? KPT : 1;
+  constexpr int kHeld = KPT > 0 ? KPT : 1;
+  uint32_t held[kHeld];
+  if constexpr (KPT > 0) {
+    float x[kHeld];
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) x[j] = w0 + 32 * j + lane < w1 ? __ldg(w + w0 + 32 * j + lane) : 0.f;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) held[j] = weight_key(x[j]);
+  }
+  // the key of this lane in sweep j (position w0 + 32 j + lane, below w1)
+  auto key_of = [&](int j) -> uint32_t {
+    if constexpr (KPT > 0) return held[j];
+    else return weight_key(__ldg(w + w0 + 32 * j + lane));
+  };
+  auto meet = [&] {
+    if (cl > 1) cluster_meet();
+    else __syncthreads();
+  };
+  for (int e = tid; e < 3 * kBins; e += kThreads) hist[0][e] = 0;
+  __syncthreads();
   uint32_t prefix = 0;
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int e = tid; e < 256; e += kThreads) hist[e] = 0;
-      __syncthreads();
-      const uint32_t fixed = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int64_t i = lo + tid; i < hi; i += kThreads) {
-        const uint32_t key = weight_key(__ldg(w + i));
-        if ((key & fixed) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
+  int need = chosen;
+  if (chosen > 0) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+      const uint32_t fixed = pass == 0 ? 0u : 0xFFFFFFFFu << (pass == 1 ? 21 : 10);
+      int* const own = hist[pass];
+#pragma unroll(kUnroll)
+      for (int j = 0; j < sweeps; ++j) {
+        const int i = w0 + 32 * j + lane;
+        bool count = i < w1 && i >= lo && i < hi;
+        const uint32_t key = count ? key_of(j) : 0u;
+        count = count && (key & fixed) == prefix;
+        const uint32_t bin = (key >> shift) & digit;
+        // (a warp whose keys all fall into one bin adds once)
+        const uint32_t in = __ballot_sync(0xFFFFFFFFu, count);
+        if (in != 0u) {
+          const int leader = __ffs(in) - 1;
+          const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, bin, leader);
+          if (__all_sync(0xFFFFFFFFu, !count || bin == b0)) {
+            if (lane == leader) atomicAdd(&own[bin], __popc(in));
+          } else if (count) {
+            atomicAdd(&own[bin], 1);
+          }
+        }
       }
+      meet();
+      if (cl > 1) {
+        // every CTA adds up its share of the bins and hands the sums to all
+        const int share = kBins / cl;
+        for (int e = rank * share + tid; e < (rank + 1) * share; e += kThreads) {
+          int sum = 0;
+          for (int r = 0; r < cl; ++r) sum += cluster_load(mapa_shared(smem_u32(&own[e]), r));
+          for (int r = 0; r < cl; ++r)
+            st_shared_cluster_u32(mapa_shared(smem_u32(&all[e]), r), static_cast<uint32_t>(sum));
+        }
+        cluster_meet();
+      }
+      // digits from the top: the one in which the need-th key lies (two bins per thread)
+      const int* counted = cl > 1 ? all : own;
+      const int c0 = counted[kBins - 1 - 2 * tid], c1 = counted[kBins - 2 - 2 * tid];
+      const int incl = warp_scan(c0 + c1);
+      if (lane == 31) warp_sum[warp] = incl;
       __syncthreads();
-      // digits from the top: the one in which the need-th key lies
-      const int mine = tid < 256 ? hist[255 - tid] : 0;
-      int sum;
-      const int above = block_prefix(mine, sh, sum);
-      if (tid < 256 && above < need && above + mine >= need) {
-        pick[0] = 255 - tid;
+      const int sums = warp_scan(warp_sum[lane]);
+      const int before = __shfl_sync(0xFFFFFFFFu, sums, (warp + 31) & 31);
+      int above = incl - c0 - c1 + (warp > 0 ? before : 0);
+      if (above < need && above + c0 >= need) {
+        pick[0] = kBins - 1 - 2 * tid;
+        pick[1] = above;
+      }
+      above += c0;
+      if (above < need && above + c1 >= need) {
+        pick[0] = kBins - 2 - 2 * tid;
         pick[1] = above;
       }
       __syncthreads();
       prefix |= static_cast<uint32_t>(pick[0]) << shift;
       need -= pick[1];
-      __syncthreads();
     }
   }
-  // `need` of the keys equal to `prefix` stay, the first ones
-  const bool any = a.budget - a.sinks - a.recent > 0;
-  int out = 0, equal = 0;
-  for (int64_t i0 = 0; i0 < n; i0 += kThreads) {
-    const int64_t i = i0 + tid;
-    float x = 0.f;
-    bool in = false, eq = false;
-    if (i < n) {
-      x = __ldg(w + i);
-      if (i < lo || i >= hi) {
-        in = true;
-      } else if (any) {
-        const uint32_t key = weight_key(x);
-        in = key > prefix;
-        eq = key == prefix;
-      }
-    }
-    int sum;
-    const int e = block_prefix(eq, sh, sum);
-    if (eq && equal + e < need) in = true;
-    equal += sum;
-    const int at = block_prefix(in, sh, sum);
-    if (in) {
-      keep[out + at] = static_cast<int32_t>(i);
-      wo[out + at] = x;
-    }
-    out += sum;
+  // `need` of the keys equal to `prefix` stay, the first ones.  Every key's class: kept for
+  // sure (2), equal (1), gone (0).
+  auto class_of = [&](int j) {
+    const int i = w0 + 32 * j + lane;
+    if (i >= w1) return 0;
+    if (i < lo || i >= hi) return 2;
+    if (chosen == 0) return 0;
+    const uint32_t key = key_of(j);
+    return key > prefix ? 2 : key == prefix ? 1 : 0;
+  };
+  int n_in = 0, n_eq = 0;
+#pragma unroll(kUnroll)
+  for (int j = 0; j < sweeps; ++j) {
+    const int c = class_of(j);
+    n_in += __popc(__ballot_sync(0xFFFFFFFFu, c == 2));
+    n_eq += __popc(__ballot_sync(0xFFFFFFFFu, c == 1));
   }
+  if (lane == 0) {
+    warp_sum[warp] = n_in;
+    warp_eq[warp] = n_eq;
+  }
+  __syncthreads();
+  const int in_scan = warp_scan(warp_sum[lane]), eq_scan = warp_scan(warp_eq[lane]);
+  int in_before = __shfl_sync(0xFFFFFFFFu, in_scan, (warp + 31) & 31);
+  int eq_before = __shfl_sync(0xFFFFFFFFu, eq_scan, (warp + 31) & 31);
+  if (warp == 0) in_before = eq_before = 0;
+  if (tid == 31) {
+    counts[0] = in_scan;
+    counts[1] = eq_scan;
+  }
+  meet();
+  for (int r = 0; r < rank; ++r) {
+    in_before += cluster_load(mapa_shared(smem_u32(&counts[0]), r));
+    eq_before += cluster_load(mapa_shared(smem_u32(&counts[1]), r));
+  }
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll(kUnroll)
+  for (int j = 0; j < sweeps; ++j) {
+    const int i = w0 + 32 * j + lane;
+    const int c = class_of(j);
+    const uint32_t eq = __ballot_sync(0xFFFFFFFFu, c == 1);
+    // place among the kept: all sure ones and the needed equal ones before it
+    const int eq_at = eq_before + __popc(eq & below);
+    const uint32_t in = __ballot_sync(0xFFFFFFFFu, c == 2);
+    if (c == 2 || (c == 1 && eq_at < need)) {
+      const int at = in_before + __popc(in & below) + min(eq_at, need);
+      keep[at] = i;
+      wo[at] = __ldg(w + i);  // (its own bits: -0 and every NaN share a key)
+    }
+    in_before += __popc(in);
+    eq_before += __popc(eq);
+  }
+  meet();  // (no CTA leaves while another may read its counts)
 }
 
-constexpr int kRows = 8;
+// One CTA per kRows output rows of a sequence; a thread keeps its 16-byte column of a row and
+// takes every 256-th, four rows at once.
+constexpr int kRows = 16;
+template <int kN>
+__device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* __restrict__ dst,
+                                          const int32_t* __restrict__ keep, int budget, int HK,
+                                          int per_head, int i0, int rows) {
+  const int per_row = HK * per_head;
+  for (int p = threadIdx.x; p < per_row; p += 256) {
+    const int32_t* kp = keep + static_cast<int64_t>(p / per_head) * budget + i0;
+    for (int r = 0; r < rows; r += kN) {
+      int64_t from[kN];
+      uint4 x[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (r + e < rows) from[e] = __ldg(kp + r + e);
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (r + e < rows) x[e] = __ldg(src + from[e] * per_row + p);
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (r + e < rows) dst[static_cast<int64_t>(i0 + r + e) * per_row + p] = x[e];
+    }
+  }
+}
 __global__ void __launch_bounds__(256) evict_copy_kernel(const Args a) {
   const int b = blockIdx.y;
+  wait_previous_kernel();
   const int n_out = static_cast<int>(min64(max64(static_cast<int64_t>(__ldg(a.lens + b)), 0),
                                            min64(a.S, a.budget)));
   const int i0 = blockIdx.x * kRows, rows = min(kRows, n_out - i0);
   if (rows <= 0) return;
-  const int pk = a.HK * a.kp, pv = a.HK * a.vp;
-  auto copy = [&](const uint4* src, uint4* dst, int per_head, int per_row) {
-    for (int e = threadIdx.x; e < rows * per_row; e += 256) {
-      const int i = i0 + e / per_row, p = e % per_row, hk = p / per_head;
-      const int64_t from = __ldg(a.keep + (static_cast<int64_t>(b) * a.HK + hk) * a.budget + i);
-      dst[(static_cast<int64_t>(b) * a.So + i) * per_row + p] =
-          __ldg(src + (static_cast<int64_t>(b) * a.S + from) * per_row + p);
-    }
-  };
-  copy(a.k, a.ko, a.kp, pk);
-  copy(a.v, a.vo, a.vp, pv);
+  const int32_t* keep = a.keep + static_cast<int64_t>(b) * a.HK * a.budget;
+  const int64_t pk = static_cast<int64_t>(a.HK) * a.kp, pv = static_cast<int64_t>(a.HK) * a.vp;
+  copy_rows<4>(a.k + b * a.S * pk, a.ko + b * a.So * pk, keep, a.budget, a.HK, a.kp, i0, rows);
+  copy_rows<4>(a.v + b * a.S * pv, a.vo + b * a.So * pv, keep, a.budget, a.HK, a.vp, i0, rows);
 }
 
 }  // namespace evict
@@ -228,12 +354,29 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
   a.sinks = p->sinks;
   a.recent = p->recent;
   a.status = p->dev_status;
-  evict::evict_select_kernel<<<static_cast<unsigned>(p->B * p->HK), evict::kThreads, 0, st>>>(a);
-  rc = check_launch("eviction select kernel launch");
+  // A row is spread over more CTAs while its slices are long, as long as all clusters run at
+  // once (32 rows of 65536 over 256 CTAs: 56 us; one row's cluster alone takes 20), or until a
+  // slice fits in registers.
+  a.cluster = 1;
+  while (a.cluster < evict::kMaxCluster &&
+         (static_cast<int64_t>(a.cluster) * 2 * evict::kSlice < p->S ||
+          (static_cast<int64_t>(a.cluster) * evict::kSlice < p->S &&
+           BH * a.cluster * 2 <= evict::kMaxCtas)))
+    a.cluster *= 2;
+  if (BH * a.cluster > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
+  // keys per thread: a warp's stretch of the longest slice, in whole 32s
+  const int64_t slice = ((p->S + a.cluster - 1) / a.cluster + 31) / 32 * 32;
+  const int64_t stretch = ((slice + evict::kWarps - 1) / evict::kWarps + 31) / 32;
+  auto select = stretch <= 4    ? evict::evict_select_kernel<4>
+                : stretch <= 8  ? evict::evict_select_kernel<8>
+                : stretch <= 16 ? evict::evict_select_kernel<16>
+                                : evict::evict_select_kernel<0>;
+  rc = launch_early(select, dim3(static_cast<unsigned>(BH * a.cluster)), dim3(evict::kThreads), 0, st,
+                    "eviction select kernel launch", a.cluster, a);
   if (rc) return rc;
   const int64_t most = min64(p->budget, p->S);
-  evict::evict_copy_kernel<<<dim3(static_cast<unsigned>((most + evict::kRows - 1) / evict::kRows),
-                                  static_cast<unsigned>(p->B)),
-                             256, 0, st>>>(a);
-  return check_launch("eviction copy kernel launch");
+  return launch_early(evict::evict_copy_kernel,
+                      dim3(static_cast<unsigned>((most + evict::kRows - 1) / evict::kRows),
+                           static_cast<unsigned>(p->B)),
+                      dim3(256), 0, st, "eviction copy kernel launch", 1, a);
 }

@@ -69,20 +69,24 @@ inline int check_launch(const char* what) { return cuda_error(cudaGetLastError()
 
 // Launches `kern` so that it may start before the kernel ahead of it in the stream has ended
 // (it waits for that kernel itself, wait_previous_kernel()): its launch and set-up overlap
-// that kernel's end.
+// that kernel's end.  `cluster`: CTAs of a cluster (along x).
 template <class... P, class... A>
 inline int launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                        const char* what, const A&... args) {
+                        const char* what, int cluster, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cuda_error(cudaLaunchKernelEx(&cfg, kern, args...), what);
 }
 

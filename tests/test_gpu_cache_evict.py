@@ -84,6 +84,11 @@ CASES = {
     "odd_d256": dict(lens=[1500, 1023, 1025], HK=2, D=D256, S=1500, budget=999, sinks=1, recent=0),
     "one_less": dict(lens=[4096, 4097], HK=1, D=D64, S=4097, budget=4096),
     "long": dict(lens=[70001, 140000], HK=1, D=D64, S=140000, budget=20011, sinks=4, recent=100),
+    "spread_over_eight": dict(lens=[60001, 33000, 9], HK=2, D=D64, S=60001, budget=7001, sinks=4, recent=1001),
+    "spread_over_four_ties": dict(lens=[16384, 14000], HK=2, D=D64, S=16384, budget=9001, sinks=0, recent=3,
+                                  weights=lambda rng, s: ties(rng, s)),
+    "longer_than_registers": dict(lens=[140001, 100000], HK=1, D=D64, S=150000, budget=30000, sinks=4, recent=100,
+                                  weights=lambda rng, s: ties(rng, s)),
     "ties": dict(lens=[5000, 3333], HK=2, D=D64, S=5000, budget=1700, sinks=4, recent=64, weights=ties),
     "all_equal": dict(lens=[5000, 2000], HK=2, D=D64, S=5000, budget=700, sinks=2, recent=3, weights=equal),
     "signed_zeros": dict(lens=[900], HK=2, D=D64, S=900, budget=300, weights=zeros),
