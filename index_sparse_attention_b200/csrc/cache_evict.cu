@@ -40,6 +40,7 @@ struct Args {
   int64_t S, So;
   int budget, sinks, recent;
   int cluster;
+  int rows;  // of a CTA of the copy
   int32_t* status;
 };
 
@@ -168,8 +169,12 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
         // every CTA adds up its share of the bins and hands the sums to all
         const int share = kBins / cl;
         for (int e = rank * share + tid; e < (rank + 1) * share; e += kThreads) {
-          int sum = 0;
-          for (int r = 0; r < cl; ++r) sum += cluster_load(mapa_shared(smem_u32(&own[e]), r));
+          int part[kMaxCluster], sum = 0;  // (all loads in flight)
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            part[r] = r < cl ? cluster_load(mapa_shared(smem_u32(&own[e]), r)) : 0;
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) sum += part[r];
           for (int r = 0; r < cl; ++r)
             st_shared_cluster_u32(mapa_shared(smem_u32(&all[e]), r), static_cast<uint32_t>(sum));
         }
@@ -229,9 +234,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
     counts[1] = eq_scan;
   }
   meet();
-  for (int r = 0; r < rank; ++r) {
-    in_before += cluster_load(mapa_shared(smem_u32(&counts[0]), r));
-    eq_before += cluster_load(mapa_shared(smem_u32(&counts[1]), r));
+  if (rank > 0) {  // lane r asks CTA r, all in flight
+    const int c = lane < rank ? cluster_load(mapa_shared(smem_u32(&counts[0]), lane)) : 0;
+    const int e = lane < rank ? cluster_load(mapa_shared(smem_u32(&counts[1]), lane)) : 0;
+    in_before += __reduce_add_sync(0xFFFFFFFFu, c);
+    eq_before += __reduce_add_sync(0xFFFFFFFFu, e);
   }
   const uint32_t below = (1u << lane) - 1u;
 #pragma unroll(kUnroll)
@@ -253,9 +260,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
   meet();  // (no CTA leaves while another may read its counts)
 }
 
-// One CTA per kRows output rows of a sequence; a thread keeps its 16-byte column of a row and
-// takes every 256-th, four rows at once.
-constexpr int kRows = 16;
+// One CTA per a.rows output rows of a sequence; a thread keeps its 16-byte column of a row and
+// takes every 256-th, four rows at once (with eight pieces of K and V mixed per thread, and a
+// quotient for each, the large copies took half as long again).
 template <int kN>
 __device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* __restrict__ dst,
                                           const int32_t* __restrict__ keep, int budget, int HK,
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const Args a) {
   wait_previous_kernel();
   const int n_out = static_cast<int>(min64(max64(static_cast<int64_t>(__ldg(a.lens + b)), 0),
                                            min64(a.S, a.budget)));
-  const int i0 = blockIdx.x * kRows, rows = min(kRows, n_out - i0);
+  const int i0 = blockIdx.x * a.rows, rows = min(a.rows, n_out - i0);
   if (rows <= 0) return;
   const int32_t* keep = a.keep + static_cast<int64_t>(b) * a.HK * a.budget;
   const int64_t pk = static_cast<int64_t>(a.HK) * a.kp, pv = static_cast<int64_t>(a.HK) * a.vp;
@@ -354,6 +361,9 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
   a.sinks = p->sinks;
   a.recent = p->recent;
   a.status = p->dev_status;
+  // rows of a copy CTA: 16, or 4 (one round of loads) where that leaves SMs without work
+  const int64_t most = min64(p->budget, p->S);
+  a.rows = (most + 15) / 16 * p->B >= 4 * 148 ? 16 : 4;
   // A row is spread over more CTAs while its slices are long, as long as all clusters run at
   // once (32 rows of 65536 over 256 CTAs: 56 us; one row's cluster alone takes 20), or until a
   // slice fits in registers.
@@ -374,9 +384,8 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
   rc = launch_early(select, dim3(static_cast<unsigned>(BH * a.cluster)), dim3(evict::kThreads), 0, st,
                     "eviction select kernel launch", a.cluster, a);
   if (rc) return rc;
-  const int64_t most = min64(p->budget, p->S);
   return launch_early(evict::evict_copy_kernel,
-                      dim3(static_cast<unsigned>((most + evict::kRows - 1) / evict::kRows),
+                      dim3(static_cast<unsigned>((most + a.rows - 1) / a.rows),
                            static_cast<unsigned>(p->B)),
                       dim3(256), 0, st, "eviction copy kernel launch", 1, a);
 }
