@@ -281,13 +281,21 @@ __global__ void __launch_bounds__(352, 1)
       // both warps have read their S columns past this barrier: P may be written over them
       named_bar_sync(pair_bar, 64);
       mx = fmaxf(xch[r], xch[128 + r]);
+      // P V of the tile before.  Every tile waits for it, here or below: a wait by parity is
+      // only right for the phase that the barrier is in, and S of a tile runs ahead of P V of
+      // the one before, whose V may be late.
+      bool waited = it == 0;
+      auto pv_done = [&]() -> bool {
+        waited = true;
+        return both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), (it - 1) & 1, ctl, a.status,
+                                                      a.wait_limit_ns)));
+      };
       const bool need = active && mx > m_run + 8.0f;
       const float alpha = need ? ex2(m_run - mx) : 1.f;
       if (__any_sync(0xFFFFFFFFu, need)) {
-        if (!first) {  // O holds P V up to the tile before: rescale this warp's O columns
-          if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), (it - 1) & 1, ctl, a.status,
-                                                      a.wait_limit_ns))))
-            return false;
+        // O holds P V up to the tile before: rescale this warp's O columns
+        if (!first) {
+          if (!pv_done()) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(352, 1)
           else tmem_st4(at, src);
         }
       }
-      return true;
+      return waited || pv_done();
     };
     for (int it = 0; it < n_iter; ++it) {
       const bool rep = (w.prefix ? a.rep_p : a.rep_c) > 1;

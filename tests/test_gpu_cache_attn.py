@@ -90,6 +90,32 @@ CASES = {
     "sharp": dict(lens=[500, 333], HQ=8, HK=2, D=D128, P=300, kscale=12.0),
 }
 
+# many tiles in a row for every SM, on memory that no cache holds yet
+LONG = {
+    "long_d64": dict(lens=[30001, 20000, 25000], HQ=16, HK=4, D=D64),
+    "long_d128": dict(lens=[30001, 20000, 25000], HQ=16, HK=4, D=D128),
+    "long_d192": dict(lens=[10001, 9000, 12345], HQ=16, HK=4, D=D192),
+    "long_d256": dict(lens=[10001, 9000, 12345], HQ=8, HK=4, D=D256),
+    "long_prefix_d128": dict(lens=[1, 300, 7], HQ=16, HK=4, D=D128, P=40001),
+    "long_prefix_d256": dict(lens=[1, 300, 7], HQ=32, HK=2, D=D256, P=20001),
+    "long_prefix_d192": dict(lens=[100, 3000, 7], HQ=64, HK=2, D=D192, P=20001),
+}
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_long_rows_on_cold_memory(name):
+    import torch
+    import index_sparse_attention_b200 as sa
+    c = Case(seed=300, **LONG[name])
+    ref, tol = c.reference(weights=False)
+    for _ in range(3):
+        g = {k: x.clone() for k, x in c.g.items()}
+        torch.empty(1 << 28, dtype=torch.uint8, device="cuda").zero_()  # (larger than L2)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = sa.cache_attn_fwd(**g, dev_status=status)
+        _compare(got, ref[:2], tol[:2])
+        assert int(status.item()) == 0
+
 
 @pytest.mark.parametrize("name", CASES)
 def test_matches_the_reference(name):
