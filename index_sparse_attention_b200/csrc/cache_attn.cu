@@ -37,7 +37,7 @@ struct Cfg {
   // (what find_range needs lies there too: every warp is past it when the first part ends)
   static constexpr int kFindOff = kMergeOff;
   static constexpr int kBarOff = kMergeOff + 32 * 1024;
-  static constexpr int kSmem = kBarOff + 256 + 1024;
+  static constexpr int kSmem = kBarOff + 272 + 1024;
   static constexpr int kThreads = 352;
   static constexpr uint32_t kOCol = 256;  // S / P buffers at columns 0 and 128
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -45,7 +45,7 @@ struct Cfg {
 };
 
 enum : int { kBQF = 0, kBQE = 2, kBKF = 4, kBKE = 9, kBVF = 14, kBVE = 19, kBSF = 24, kBPF = 26,
-             kBOD = 28, kBDrain = 29, kNumBars = 30 };
+             kBOD = 28, kBDrain = 29, kBOF = 30, kNumBars = 31 };
 
 // maps: Q for prefix row tiles and for one sequence, K / V of the prefix and of the caches
 struct Maps {
@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(352, 1)
                   (!first_o || kk > 0) ? 1u : 0u);
         umma_commit(BAR(kBOD));
         umma_commit(BAR(kBVE + vs));
+        if (last) umma_commit(BAR(kBOF));  // the part's O is complete
       }
       __syncwarp();
       if (it + 1 < n_iter) first_o = wo.next(a);
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(352, 1)
     const int r = quarter * 32 + lane;
     float m_run = -INFINITY, l_run = 0.f;
     bool first = true, ok = true;
+    int part = 0;
     auto both = [&](bool v) { return named_bar_and(pair_bar, 64, v); };
     // One tile: S columns [c0, c0 + NC) of this thread's row -> P.  kRep: the row's copy in
     // this quarter takes the quarter's kN / 4 columns, the others' P is zero.
@@ -281,21 +283,16 @@ __global__ void __launch_bounds__(352, 1)
       // both warps have read their S columns past this barrier: P may be written over them
       named_bar_sync(pair_bar, 64);
       mx = fmaxf(xch[r], xch[128 + r]);
-      // P V of the tile before.  Every tile waits for it, here or below: a wait by parity is
-      // only right for the phase that the barrier is in, and S of a tile runs ahead of P V of
-      // the one before, whose V may be late.
-      bool waited = it == 0;
-      auto pv_done = [&]() -> bool {
-        waited = true;
-        return both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), (it - 1) & 1, ctl, a.status,
-                                                      a.wait_limit_ns)));
-      };
       const bool need = active && mx > m_run + 8.0f;
       const float alpha = need ? ex2(m_run - mx) : 1.f;
       if (__any_sync(0xFFFFFFFFu, need)) {
-        // O holds P V up to the tile before: rescale this warp's O columns
+        // O holds P V up to the tile before: rescale this warp's O columns.  (A wait by parity
+        // needs the barrier in that phase or the next: P V of tile it - 2 was queued before
+        // S of tile it, which is done, and P V of this tile waits for the P below.)
         if (!first) {
-          if (!pv_done()) return false;
+          if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), (it - 1) & 1, ctl, a.status,
+                                                      a.wait_limit_ns))))
+            return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
@@ -339,7 +336,7 @@ __global__ void __launch_bounds__(352, 1)
           else tmem_st4(at, src);
         }
       }
-      return waited || pv_done();
+      return true;
     };
     for (int it = 0; it < n_iter; ++it) {
       const bool rep = (w.prefix ? a.rep_p : a.rep_c) > 1;
@@ -377,7 +374,11 @@ __global__ void __launch_bounds__(352, 1)
       if (first) {
         // ------------------------------------------------------------ a part ends
         if (ok)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOD), it & 1, ctl, a.status, a.wait_limit_ns));
+          // (a barrier of its own, one phase per part: P V of the tile before may still wait for
+          // its V here, and the other barrier would then be a phase early)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOF), part & 1, ctl, a.status,
+                                                 a.wait_limit_ns));
+        ++part;
         ok = named_bar_and(8, 256, ok);
         if (!ok) continue;
         tc_fence_after();
