@@ -18,7 +18,9 @@ namespace cache {
 template <int DQK, int DV>
 struct Cfg {
   static constexpr int kN = DQK <= 128 ? 128 : 64;  // keys of a tile
-  static constexpr int kQStages = DQK == 256 ? 1 : 2;
+  // Q buffers: part p uses buffer p % 2; at head dims 256 there is one, in which the copies of up
+  // to 16 rows take rows [0, 16) or [16, 32) of each lane quarter by turns
+  static constexpr int kQBufs = DQK == 256 ? 1 : 2;
   static constexpr int kKStages = DQK == 64 ? 5 : 2;  // (a third one measured no faster)
   static constexpr int kVStages = DQK == 64 ? 5 : DQK == 192 ? 3 : 2;
   static constexpr int kQPanel = 128 * 128;  // 64 columns x 128 rows
@@ -26,7 +28,7 @@ struct Cfg {
   static constexpr int kQBytes = 128 * DQK * 2;
   static constexpr int kKBytes = kN * DQK * 2;
   static constexpr int kVBytes = kN * DV * 2;
-  static constexpr int kKOff = kQStages * kQBytes;
+  static constexpr int kKOff = kQBufs * kQBytes;
   static constexpr int kVOff = kKOff + kKStages * kKBytes;
   // what the two warps of a quarter exchange, [2][128]: a tile's row maxima, a part's row sums
   // (a barrier of the pair lies between one use's reads and the next one's writes)
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(352, 1)
         const int n = __ldg(a.lens + b);
         if (n < 0 || n > a.S) report_status(a.status, kStatusIndex);
       }
-    bool first = true;
+    bool first = true, was_full = false;
     for (int it = 0; it < n_iter; ++it) {
       const int ks = it % C::kKStages, ku = it / C::kKStages;
       if (!warp_wait(BAR(kBKE + ks), (ku & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
@@ -121,16 +123,23 @@ __global__ void __launch_bounds__(352, 1)
       __syncwarp();
       issued_k = it + 1;
       if (first) {
-        const int qs = issued_q % C::kQStages, qu = issued_q / C::kQStages;
+        const int qs = issued_q & 1, qu = issued_q >> 1;
+        const int rep = w.prefix ? a.rep_p : a.rep_c, rows = w.prefix ? a.rows_p : a.rows_c;
+        const bool full = rep == 1 || rows > 16;  // (a whole buffer)
         if (!warp_wait(BAR(kBQE + qs), (qu & 1) ^ 1, ctl, a.status, a.wait_limit_ns)) break;
+        // one buffer: a part that takes all of it, or follows one that does, waits for that too
+        if (C::kQBufs == 1 && issued_q > 0 && (full || was_full) &&
+            !warp_wait(BAR(kBQE + (qs ^ 1)), ((issued_q - 1) >> 1) & 1, ctl, a.status,
+                       a.wait_limit_ns))
+          break;
+        was_full = full;
         if (elect_one()) {
-          const int rep = w.prefix ? a.rep_p : a.rep_c, rows = w.prefix ? a.rows_p : a.rows_c;
           mbar_arrive_expect_tx(BAR(kBQF + qs), rep * rows * DQK * 2);
+          const uint32_t dst = sbase + (C::kQBufs == 2 ? qs * C::kQBytes : full ? 0 : qs * 16 * 128);
           for (int r = 0; r < rep; ++r)
             for (int c = 0; c < DQK / 64; ++c)
-              tma_load_4d(sbase + qs * C::kQBytes + c * C::kQPanel + r * 32 * 128,
-                          w.prefix ? &maps.qp : &maps.qc, BAR(kBQF + qs), c * 64,
-                          w.prefix ? w.rt * a.nb : w.b, w.hk * a.G, 0);
+              tma_load_4d(dst + c * C::kQPanel + r * 32 * 128, w.prefix ? &maps.qp : &maps.qc,
+                          BAR(kBQF + qs), c * 64, w.prefix ? w.rt * a.nb : w.b, w.hk * a.G, 0);
         }
         __syncwarp();
         ++issued_q;
@@ -143,10 +152,8 @@ __global__ void __launch_bounds__(352, 1)
         if (!warp_wait(BAR(kBKE + it % C::kKStages), (it / C::kKStages) & 1, ctl, a.status,
                        a.wait_limit_ns))
           break;
-      for (int q = max(0, issued_q - C::kQStages); q < issued_q; ++q)
-        if (!warp_wait(BAR(kBQE + q % C::kQStages), (q / C::kQStages) & 1, ctl, a.status,
-                       a.wait_limit_ns))
-          break;
+      for (int q = max(0, issued_q - 2); q < issued_q; ++q)
+        if (!warp_wait(BAR(kBQE + (q & 1)), (q >> 1) & 1, ctl, a.status, a.wait_limit_ns)) break;
     }
   } else if (warp == 10) {
     // ---------------------------------------------------------------- V producer
@@ -179,14 +186,14 @@ __global__ void __launch_bounds__(352, 1)
     Walk wo = w;                  // the walk of the P V being issued (one tile behind)
     auto issue_s = [&](int it) -> bool {
       const int ks = it % C::kKStages, ku = it / C::kKStages;
-      const int qs = part % C::kQStages, qu = part / C::kQStages;
+      const int qs = part & 1, qu = part >> 1;
       if (first_s && !warp_wait(BAR(kBQF + qs), qu & 1, ctl, a.status, a.wait_limit_ns)) return false;
       if (!warp_wait(BAR(kBKF + ks), ku & 1, ctl, a.status, a.wait_limit_ns)) return false;
       tc_fence_after();
       const bool more = it + 1 < n_iter;
       const bool ends = !more || w.next(a);  // the part's last tile
       const uint64_t kd = sw128_desc(sbase + C::kKOff + ks * C::kKBytes, 16, 1024);
-      const uint64_t qd = sw128_desc(sbase + qs * C::kQBytes, 16, 1024);
+      const uint64_t qd = sw128_desc(sbase + (C::kQBufs == 2 ? qs * C::kQBytes : 0), 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < DQK / 16; ++kk)
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(352, 1)
     auto both = [&](bool v) { return named_bar_and(pair_bar, 64, v); };
     // One tile: S columns [c0, c0 + NC) of this thread's row -> P.  kRep: the row's copy in
     // this quarter takes the quarter's kN / 4 columns, the others' P is zero.
-    auto tile = [&](auto nc, bool rep, int it, bool active) -> bool {
+    auto tile = [&](auto nc, bool rep, int it, bool active, int loff) -> bool {
       constexpr int NC = decltype(nc)::value;
       const int sb = it & 1;
       const uint32_t scol = tl + sb * 128;
@@ -261,24 +268,33 @@ __global__ void __launch_bounds__(352, 1)
       tmem_wait_ld();
       float x[NC];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(u[c]) * a.scale_log2;
+      for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(u[c]);
       if (lim < kN) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
           if (c0 + c >= lim) x[c] = -INFINITY;
       }
+      const float sc = a.scale_log2;
       if (a.scores && !w.prefix && active) {
-        const int g = rep ? lane : r;
+        const int g = rep ? lane - loff : r;
         float4* dst = reinterpret_cast<float4*>(
             a.scores + (static_cast<int64_t>(w.b) * a.HQ + w.hk * a.G + g) * a.Sp + k0 + c0);
 #pragma unroll
         for (int e = 0; e < NC / 4; ++e)
-          dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          dst[e] = make_float4(x[4 * e] * sc, x[4 * e + 1] * sc, x[4 * e + 2] * sc,
+                               x[4 * e + 3] * sc);
       }
       float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 4; c < NC; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], x[c]);
-      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      for (int c = 4; c + 4 < NC; c += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx4[e] = max3(mx4[e], x[c + e], x[c + 4 + e]);
+      }
+      if constexpr (NC % 8 == 0) {  // (four are left over)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], x[NC - 4 + e]);
+      }
+      float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * sc;
       xch[hc * 128 + r] = mx;
       // both warps have read their S columns past this barrier: P may be written over them
       named_bar_sync(pair_bar, 64);
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(352, 1)
       uint32_t pk[NC / 2];
 #pragma unroll
       for (int e = 0; e < NC / 2; ++e) {
-        const float p0 = ex2(x[2 * e] - m_eff), p1 = ex2(x[2 * e + 1] - m_eff);
+        const float p0 = ex2(fmaf(x[2 * e], sc, -m_eff)), p1 = ex2(fmaf(x[2 * e + 1], sc, -m_eff));
         ps[e & 3] += p0 + p1;
         pk[e] = pack_bf16x2(p0, p1);
       }
@@ -341,12 +357,15 @@ __global__ void __launch_bounds__(352, 1)
     for (int it = 0; it < n_iter; ++it) {
       const bool rep = (w.prefix ? a.rep_p : a.rep_c) > 1;
       const int rows = w.prefix ? a.rows_p : a.rows_c;
-      const bool active = (rep ? lane : r) < rows;
+      // where the copies' rows begin in each lane quarter
+      const int loff = C::kQBufs == 1 && rep && rows <= 16 ? 16 * (part & 1) : 0;
+      const int mine = rep ? lane - loff : r;
+      const bool active = mine >= 0 && mine < rows;
       // (after a wait that gave up the loop goes on without work, so that the warps still meet
       // at the barriers of a part's end)
       if (ok)
-        ok = rep ? tile(std::integral_constant<int, kN / 8>{}, true, it, active)
-                 : tile(std::integral_constant<int, kN / 2>{}, false, it, active);
+        ok = rep ? tile(std::integral_constant<int, kN / 8>{}, true, it, active, loff)
+                 : tile(std::integral_constant<int, kN / 2>{}, false, it, active, 0);
       const int lim = static_cast<int>(min64(kN, w.keys - w.tile * kN));
       if (ok && !w.prefix && lim < kN) {
         // the V rows behind the sequence hold anything, and 0 x NaN is NaN: clear them
@@ -416,7 +435,7 @@ __global__ void __launch_bounds__(352, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               l += (xch[32 * q + lane] + xch[128 + 32 * q + lane]) * ex2(xm[32 * q + lane] - me);
-            mls[lane] = make_float2(mm, l);
+            mls[mine] = make_float2(mm, l);
           }
           // up to eight rows: all columns of this half at once, else 32 at a time
           float* stage = reinterpret_cast<float*>(smem + C::kMergeOff + hc * 16384);
@@ -430,10 +449,10 @@ __global__ void __launch_bounds__(352, 1)
               tmem_ld32(tl + C::kOCol + c0 + c, ov);
               tmem_wait_ld();
               if (active) {
-                float4* dst = reinterpret_cast<float4*>(stage + (quarter * rows + lane) * cp + c);
+                float4* dst = reinterpret_cast<float4*>(stage + (quarter * rows + mine) * cp + c);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  dst[e ^ (lane & 7)] = make_float4(
+                  dst[e ^ (mine & 7)] = make_float4(
                       __uint_as_float(ov[4 * e]) * f, __uint_as_float(ov[4 * e + 1]) * f,
                       __uint_as_float(ov[4 * e + 2]) * f, __uint_as_float(ov[4 * e + 3]) * f);
               }
@@ -469,8 +488,8 @@ __global__ void __launch_bounds__(352, 1)
   // copies and MMAs in flight before shared and tensor memory are released.
   if (ctl->abort) {
     if (lane == 0 && warp == 0) {
-      for (int q = max(0, issued_q - C::kQStages); q < issued_q; ++q)
-        mbar_wait_limited(BAR(kBQF + q % C::kQStages), (q / C::kQStages) & 1);
+      for (int q = max(0, issued_q - 2); q < issued_q; ++q)
+        mbar_wait_limited(BAR(kBQF + (q & 1)), (q >> 1) & 1);
       for (int it = max(0, issued_k - C::kKStages); it < issued_k; ++it)
         mbar_wait_limited(BAR(kBKF + it % C::kKStages), (it / C::kKStages) & 1);
     }

@@ -83,6 +83,10 @@ CASES = {
     "group_48_d192": dict(lens=[140, 20, 300], HQ=48, HK=1, D=D192, P=150),
     "group_128": dict(lens=[300, 5], HQ=128, HK=1, D=D128, P=131),
     "group_128_d256": dict(lens=[300, 5], HQ=128, HK=1, D=D256, P=131),
+    "group_20_d256": dict(lens=[140, 20, 300, 7, 500], HQ=20, HK=1, D=D256, P=150),
+    "group_20_d256_many_parts": dict(lens=[3, 70, 64, 1, 90] * 60, HQ=20, HK=1, D=D256),
+    "small_parts_d256": dict(lens=[3, 70, 64, 1, 90] * 40, HQ=8, HK=2, D=D256, P=150),
+    "small_parts_full_prefix_d256": dict(lens=[9, 65], HQ=40, HK=2, D=D256, P=1000),
     "many_rows": dict(lens=[5 + 3 * i for i in range(70)], HQ=16, HK=2, D=D128, P=515),
     "many_rows_d256": dict(lens=[5 + 3 * i for i in range(40)], HQ=8, HK=1, D=D256, P=260),
     "many_sequences": dict(lens=[(7 * i) % 50 for i in range(400)], HQ=2, HK=1, D=D64, P=33),
