@@ -96,9 +96,9 @@ __global__ void __launch_bounds__(352, 1)
       a, cta, reinterpret_cast<int64_t*>(smem + C::kFindOff));  // (ends with a barrier)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  const int n_iter = static_cast<int>(f.u1 - f.u0);
+  const int n_iter = f.n;
   Walk w{};
-  if (n_iter > 0) w.init(a, f.u0, f.b, f.off);
+  if (n_iter > 0) w.init(a, f);
   int issued_k = 0, issued_v = 0, issued_q = 0;  // loads issued (the abort path drains the last)
 
   if (warp == 0) {
@@ -414,10 +414,9 @@ __global__ void __launch_bounds__(352, 1)
             tmem_ld32(tl + C::kOCol + c, ov);
             tmem_wait_ld();
             if (active) {
-              uint4* dst = reinterpret_cast<uint4*>(po + static_cast<int64_t>(r) * DV + c);
+              float* dst = po + static_cast<int64_t>(r) * DV + c;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              for (int e = 0; e < 4; ++e) st_global_v8(dst + 8 * e, ov + 8 * e);
             }
           }
         } else {
@@ -533,10 +532,10 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   if (row >= static_cast<int64_t>(a.B) * a.HQ) return;  // (kW == 1 only: a whole warp)
   const int b = static_cast<int>(row / a.HQ), h = static_cast<int>(row - static_cast<int64_t>(b) * a.HQ);
   const int hk = h / a.G, g = h - hk * a.G;
-  // tiles before this sequence and in all (every warp for itself)
+  // the plan's line up to this sequence and in all (every warp for itself)
   int64_t before = 0, total = 0;
   for (int x = lane; x < a.B; x += 32) {
-    const int64_t t = tiles_of(a, clamped_len(a, x));
+    const int64_t t = length_of(a, tiles_of(a, clamped_len(a, x)), a.wt_c);
     total += t;
     if (x < b) before += t;
   }
@@ -545,8 +544,8 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
     before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
     total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
   }
-  const int64_t np = a.Tp * a.Rt * a.HK, U = np + total * a.HK;
-  const int C = busy_ctas(a, U);
+  const int64_t np = prefix_length(a), U = np + total * a.HK;
+  const int64_t q = share_of(a, U);
   const int64_t tb = tiles_of(a, clamped_len(a, b));
   // parts of the prefix (of this row's tile) and of the own cache: rows of ml / po, `step` apart
   int n_p = 0, n_c = 0;
@@ -554,13 +553,16 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   if (np > 0) {
     const int rt = b / a.nb;
     const int64_t seg = static_cast<int64_t>(hk) * a.Rt + rt;
-    const int c0 = cta_of(seg * a.Tp, U, C), c1 = cta_of(seg * a.Tp + a.Tp - 1, U, C);
+    const int64_t x = seg * length_of(a, a.Tp, a.wt_p);
+    const int c0 = static_cast<int>(quotient(x, q));
+    const int c1 = static_cast<int>(quotient(x + (a.Tp - 1) * a.wt_p, q));
     n_p = c1 - c0 + 1;
     at_p = (seg + c0) * a.rows_p + g * a.nb + (b - rt * a.nb);
   }
   if (tb > 0) {
-    const int64_t u = np + before * a.HK + hk * tb;
-    const int c0 = cta_of(u, U, C), c1 = cta_of(u + tb - 1, U, C);
+    const int64_t x = np + before * a.HK + hk * length_of(a, tb, a.wt_c);
+    const int c0 = static_cast<int>(quotient(x, q));
+    const int c1 = static_cast<int>(quotient(x + (tb - 1) * a.wt_c, q));
     n_c = c1 - c0 + 1;
     at_c = (static_cast<int64_t>(b) * a.HK + hk + c0) * a.rows_c + g;
   }
@@ -708,16 +710,23 @@ static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
   a->Dv = p->Dv;
   a->S = p->S;
   a->P = p->P;
-  a->kn = p->Dqk <= 128 ? 128 : 64;
+  a->kshift = p->Dqk <= 128 ? 7 : 6;
   a->Sp = (p->S + 127) / 128 * 128;
   a->nb = 128 / a->G;
   if (a->nb > p->B) a->nb = p->B;
   a->Rt = (p->B + a->nb - 1) / a->nb;
-  a->Tp = (p->P + a->kn - 1) / a->kn;
+  a->Tp = (p->P + (1 << a->kshift) - 1) >> a->kshift;
   a->rows_p = a->nb * a->G;
   a->rows_c = a->G;
   a->rep_p = a->rows_p <= 32 ? 4 : 1;  // (few rows: a copy in each TMEM lane quarter)
   a->rep_c = a->rows_c <= 32 ? 4 : 1;
+  // in hundreds of cycles, measured: a tile of few rows takes what its keys take from HBM, one of
+  // many rows its exponentials
+  const int many = p->Dqk == 64 ? 22 : p->Dqk == 192 ? 19 : 27;
+  const int few = p->Dqk == 64 ? 12 : p->Dqk == 192 ? 15 : 24;
+  a->wt_p = a->rep_p > 1 ? few : many;
+  a->wt_c = a->rep_c > 1 ? few : many;
+  a->we = 30;
   const size_t parts_p = p->P ? (static_cast<size_t>(a->HK) * a->Rt + kMaxCtas) * a->rows_p : 0;
   const size_t parts_c = (static_cast<size_t>(p->B) * p->HK + kMaxCtas) * a->rows_c;
   size_t off = 0;
