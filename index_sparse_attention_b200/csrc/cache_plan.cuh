@@ -66,11 +66,13 @@ __device__ __forceinline__ int64_t prefix_length(const Args& a) {
   return length_of(a, a.Tp, a.wt_p) * a.Rt * a.HK;
 }
 // Quotient of non-negative numbers; 32-bit division where both fit (the 64-bit one takes several
-// times as long, and half a dozen of them in a row 2 us of every call).
+// times as long, and half a dozen of them in a row 2 us of every call; out of line, since its
+// copies would be most of a short kernel's code).
+static __device__ __noinline__ int64_t quotient64(int64_t x, int64_t d) { return x / d; }
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t d) {
   if ((static_cast<uint64_t>(x | d) >> 32) == 0)
     return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
-  return x / d;
+  return quotient64(x, d);
 }
 // what a CTA takes of a line of U (see above)
 __device__ __forceinline__ int64_t share_of(const Args& a, int64_t U) {
