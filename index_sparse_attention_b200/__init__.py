@@ -41,7 +41,7 @@ def _on_device(arg):
         def wrapper(*args, **kw):
             t = kw.get(arg) if arg in kw else (args[pos] if pos < len(args) else None)
             if isinstance(t, torch.Tensor) and t.is_cuda:
-                if type(t) is torch.Tensor and t.get_device() == torch.cuda.current_device():
+                if type(t) is torch.Tensor and t.get_device() == torch._C._cuda_getDevice():
                     return fn(*args, **kw)
                 with torch.cuda.device(t.device):
                     return fn(*args, **kw)
@@ -50,6 +50,10 @@ def _on_device(arg):
         wrapper.device_arg = arg
         return wrapper
     return deco
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _ptr(t):
@@ -83,6 +87,13 @@ def _check(name, t, dtype, shape=None, ndim=None, device=None, contiguous=True):
         _require(t.is_contiguous(), f"{name} must be contiguous")
     if device is not None:
         _require(t.device == device, f"{name} is on {t.device}, expected {device}")
+
+
+def _fits(t, dtype, shape, device):
+    """Whether a tensor passes _check with these (the fast way through a call's checks: one
+    expression per tensor, and _check to say what is wrong where one fails)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_cuda and t.is_contiguous())
 
 
 def _check_status(dev_status, device):
@@ -327,8 +338,8 @@ def topk_select(scores, k, starts=None, ends=None, with_values=False, out_idx=No
     return (out_idx, out_val) if with_values else out_idx
 
 
-def _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, weights, weights_out, o,
-                  lse, dev_status):
+def _check_cache_args(q, k_cache, v_cache, lens, k_prefix, v_prefix, weights, weights_out, o, lse,
+                      dev_status):
     _check("q", q, torch.bfloat16, ndim=4)
     B, T, HQ, Dqk = q.shape
     _require(T == 1, f"q must hold one token per sequence [B, 1, HQ, Dqk], got {tuple(q.shape)}")
@@ -343,14 +354,11 @@ def _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, weights,
              f"got {tuple(v_cache.shape)}")
     _check("lens", lens, torch.int32, shape=(B,), device=dev)
     _require((k_prefix is None) == (v_prefix is None), "k_prefix and v_prefix go together")
-    P = 0
     if k_prefix is not None:
         _check("k_prefix", k_prefix, torch.bfloat16, ndim=3, device=dev)
         P = k_prefix.shape[0]
         _check("k_prefix", k_prefix, torch.bfloat16, shape=(P, HK, Dqk), device=dev)
         _check("v_prefix", v_prefix, torch.bfloat16, shape=(P, HK, Dv), device=dev)
-        if P == 0:
-            k_prefix = v_prefix = None
     for name, t in (("weights", weights), ("weights_out", weights_out)):
         if t is not None:
             _check(name, t, torch.float32, shape=(B, HK, S), device=dev)
@@ -359,13 +367,49 @@ def _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, weights,
     if lse is not None:
         _check("lse", lse, torch.float32, shape=(B, HQ, 1), device=dev)
     _check_status(dev_status, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(Dqk)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+
+
+def _cache_args_fit(q, k_cache, v_cache, lens, k_prefix, v_prefix, weights, weights_out, o, lse,
+                    dev_status):
+    """Whether everything _check_cache_args looks at is as it should be."""
+    if not (isinstance(q, torch.Tensor) and q.dim() == 4 and isinstance(v_cache, torch.Tensor)
+            and v_cache.dim() == 4 and dev_status is None):
+        return False
+    bf16, dev = torch.bfloat16, q.device
+    B, T, HQ, Dqk = q.shape
+    _, S, HK, Dv = v_cache.shape
+    if not (_fits(q, bf16, (B, 1, HQ, Dqk), dev) and _fits(k_cache, bf16, (B, S, HK, Dqk), dev)
+            and _fits(v_cache, bf16, (B, S, HK, Dv), dev) and _fits(lens, torch.int32, (B,), dev)):
+        return False
+    if k_prefix is not None:
+        if not (isinstance(k_prefix, torch.Tensor) and k_prefix.dim() == 3):
+            return False
+        P = k_prefix.shape[0]
+        if not (_fits(k_prefix, bf16, (P, HK, Dqk), dev) and _fits(v_prefix, bf16, (P, HK, Dv), dev)):
+            return False
+    elif v_prefix is not None:
+        return False
+    return ((weights is None or _fits(weights, torch.float32, (B, HK, S), dev))
+            and (weights_out is None or _fits(weights_out, torch.float32, (B, HK, S), dev))
+            and (o is None or _fits(o, bf16, (B, 1, HQ, Dv), dev))
+            and (lse is None or _fits(lse, torch.float32, (B, HQ, 1), dev)))
+
+
+def _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, scale, weights, weights_out, o,
+                  lse, dev_status):
+    if not _cache_args_fit(q, k_cache, v_cache, lens, k_prefix, v_prefix, weights, weights_out, o,
+                           lse, dev_status):
+        _check_cache_args(q, k_cache, v_cache, lens, k_prefix, v_prefix, weights, weights_out, o,
+                          lse, dev_status)
+    B, _, HQ, Dqk = q.shape
+    _, S, HK, Dv = v_cache.shape
+    P = 0 if k_prefix is None else k_prefix.shape[0]
+    if P == 0:
+        k_prefix = v_prefix = None
     return _lib.CacheAttnStruct(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), ptr(k_prefix),
-        ptr(v_prefix), ptr(o), ptr(lse), ptr(weights), ptr(weights_out), B, HQ, HK, Dqk, Dv, S, P,
-        float(scale), ptr(dev_status))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lens.data_ptr(), _addr(k_prefix),
+        _addr(v_prefix), _addr(o), _addr(lse), _addr(weights), _addr(weights_out), B, HQ, HK, Dqk,
+        Dv, S, P, 1.0 / math.sqrt(Dqk) if scale is None else float(scale), _addr(dev_status))
 
 
 @_on_device("q")
@@ -395,23 +439,26 @@ def cache_attn_fwd(q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None, soft
     L = _lib.load()
     p = _cache_params(q, k_cache, v_cache, lens, k_prefix, v_prefix, softmax_scale, weights,
                       weights_out, o, lse, dev_status)
-    _require(weights is None or with_weights or weights_out is not None,
-             "weights needs with_weights or a weights_out")
+    if weights is not None and not with_weights and weights_out is None:
+        raise ValueError("weights needs with_weights or a weights_out")
+    B, HQ, HK, Dv, S, dev = p.B, p.HQ, p.HK, p.Dv, p.S, q.device
     if o is None:
-        o = torch.empty((p.B, 1, p.HQ, p.Dv), dtype=torch.bfloat16, device=q.device)
+        o = torch.empty(B, 1, HQ, Dv, dtype=torch.bfloat16, device=dev)
         p.o = o.data_ptr()
     if lse is None:
-        lse = torch.empty((p.B, p.HQ, 1), dtype=torch.float32, device=q.device)
+        lse = torch.empty(B, HQ, 1, dtype=torch.float32, device=dev)
         p.lse = lse.data_ptr()
     if with_weights and weights_out is None:
-        weights_out = torch.empty((p.B, p.HK, p.S), dtype=torch.float32, device=q.device)
+        weights_out = torch.empty(B, HK, S, dtype=torch.float32, device=dev)
         p.weights_out = weights_out.data_ptr()
+    ref = ctypes.byref(p)
     if workspace is None:
-        need = int(L.cache_attn_workspace_size(ctypes.byref(p)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check("workspace", workspace, torch.uint8, device=q.device)
-    _lib.check("cache_attn_fwd", L.cache_attn_fwd(ctypes.byref(p), _ptr(workspace),
-                                                  workspace.numel(), _stream(q.device)))
+        workspace = torch.empty(L.cache_attn_workspace_size(ref), dtype=torch.uint8, device=dev)
+    else:
+        _check("workspace", workspace, torch.uint8, device=dev)
+    code = L.cache_attn_fwd(ref, workspace.data_ptr(), workspace.numel(), _stream(dev))
+    if code:
+        _lib.check("cache_attn_fwd", code)
     return (o, lse) if weights_out is None else (o, lse, weights_out)
 
 
@@ -445,13 +492,16 @@ def sparse_attn_key_weights(q, k, lse, sparse, softmax_scale=None, weights=None,
         q.data_ptr(), k.data_ptr(), None, None, lse.data_ptr(), None, None, None, None, B, HQ, HK,
         Dqk, Dv, Sq, Sk, float(softmax_scale), ctypes.pointer(sparse.c),
         None if dev_status is None else dev_status.data_ptr())
+    ref = ctypes.byref(p)
     if workspace is None:
-        need = int(L.sparse_attn_key_weights_workspace_size(ctypes.byref(p)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check("workspace", workspace, torch.uint8, device=dev)
-    _lib.check("sparse_attn_key_weights",
-               L.sparse_attn_key_weights(ctypes.byref(p), _ptr(weights), _ptr(weights_out),
-                                         _ptr(workspace), workspace.numel(), _stream(dev)))
+        workspace = torch.empty(L.sparse_attn_key_weights_workspace_size(ref), dtype=torch.uint8,
+                                device=dev)
+    else:
+        _check("workspace", workspace, torch.uint8, device=dev)
+    code = L.sparse_attn_key_weights(ref, _addr(weights), weights_out.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel(), _stream(dev))
+    if code:
+        _lib.check("sparse_attn_key_weights", code)
     return weights_out
 
 
@@ -467,48 +517,60 @@ def cache_evict(k_cache, v_cache, weights, lens, budget, sinks=0, recent=0, k_ou
     behind the kept keys), lens_out int32 [B] and keep int32 [B,HK,budget] (the kept
     positions, then -1).  The outputs must not overlap the inputs."""
     L = _lib.load()
-    _check("k_cache", k_cache, torch.bfloat16, ndim=4)
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    _check("k_cache", k_cache, bf16, ndim=4)
     B, S, HK, Dqk = k_cache.shape
     dev = k_cache.device
-    _check("v_cache", v_cache, torch.bfloat16, ndim=4, device=dev)
+    _check("v_cache", v_cache, bf16, ndim=4, device=dev)
     Dv = v_cache.shape[3]
-    _check("v_cache", v_cache, torch.bfloat16, shape=(B, S, HK, Dv), device=dev)
-    _check("weights", weights, torch.float32, shape=(B, HK, S), device=dev)
-    _check("lens", lens, torch.int32, shape=(B,), device=dev)
+    if not (_fits(v_cache, bf16, (B, S, HK, Dv), dev) and _fits(weights, f32, (B, HK, S), dev)
+            and _fits(lens, i32, (B,), dev)):
+        _check("v_cache", v_cache, bf16, shape=(B, S, HK, Dv), device=dev)
+        _check("weights", weights, f32, shape=(B, HK, S), device=dev)
+        _check("lens", lens, i32, shape=(B,), device=dev)
     _check_status(dev_status, dev)
     budget, sinks, recent = int(budget), int(sinks), int(recent)
+    S_out = S
+    if k_out is not None:
+        _check("k_out", k_out, bf16, ndim=4, device=dev)
+        S_out = k_out.shape[1]
+        _check("k_out", k_out, bf16, shape=(B, S_out, HK, Dqk), device=dev)
+    elif v_out is not None:
+        _check("v_out", v_out, bf16, ndim=4, device=dev)
+        S_out = v_out.shape[1]
+    if not 1 <= budget <= S_out:
+        raise ValueError(f"budget must be in [1, {S_out}] (k_out's rows), got {budget}")
+    if sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("sinks and recent must be non-negative with a sum of at most "
+                         f"budget={budget}, got {sinks} and {recent}")
     if k_out is None:
-        S_out = S if v_out is None else v_out.shape[1]
-        k_out = torch.empty((B, S_out, HK, Dqk), dtype=torch.bfloat16, device=dev)
-    _check("k_out", k_out, torch.bfloat16, ndim=4, device=dev)
-    S_out = k_out.shape[1]
-    _check("k_out", k_out, torch.bfloat16, shape=(B, S_out, HK, Dqk), device=dev)
-    _require(1 <= budget <= S_out, f"budget must be in [1, {S_out}] (k_out's rows), got {budget}")
-    _require(sinks >= 0 and recent >= 0 and sinks + recent <= budget,
-             f"sinks and recent must be non-negative with a sum of at most budget={budget}, "
-             f"got {sinks} and {recent}")
+        k_out = torch.empty(B, S_out, HK, Dqk, dtype=bf16, device=dev)
     if v_out is None:
-        v_out = torch.empty((B, S_out, HK, Dv), dtype=torch.bfloat16, device=dev)
-    _check("v_out", v_out, torch.bfloat16, shape=(B, S_out, HK, Dv), device=dev)
+        v_out = torch.empty(B, S_out, HK, Dv, dtype=bf16, device=dev)
+    else:
+        _check("v_out", v_out, bf16, shape=(B, S_out, HK, Dv), device=dev)
     if weights_out is None:
-        weights_out = torch.empty((B, HK, S_out), dtype=torch.float32, device=dev)
-    _check("weights_out", weights_out, torch.float32, shape=(B, HK, S_out), device=dev)
+        weights_out = torch.empty(B, HK, S_out, dtype=f32, device=dev)
+    else:
+        _check("weights_out", weights_out, f32, shape=(B, HK, S_out), device=dev)
     if lens_out is None:
-        lens_out = torch.empty((B,), dtype=torch.int32, device=dev)
-    _check("lens_out", lens_out, torch.int32, shape=(B,), device=dev)
+        lens_out = torch.empty(B, dtype=i32, device=dev)
+    else:
+        _check("lens_out", lens_out, i32, shape=(B,), device=dev)
     if keep is None:
-        keep = torch.empty((B, HK, budget), dtype=torch.int32, device=dev)
-    _check("keep", keep, torch.int32, shape=(B, HK, budget), device=dev)
+        keep = torch.empty(B, HK, budget, dtype=i32, device=dev)
+    else:
+        _check("keep", keep, i32, shape=(B, HK, budget), device=dev)
     p = _lib.CacheEvictStruct(
         k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), lens.data_ptr(),
         k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(), lens_out.data_ptr(),
-        keep.data_ptr(), B, HK, Dqk, Dv, S, S_out, budget, sinks, recent,
-        None if dev_status is None else dev_status.data_ptr())
+        keep.data_ptr(), B, HK, Dqk, Dv, S, S_out, budget, sinks, recent, _addr(dev_status))
     code = L.cache_evict(ctypes.byref(p), _stream(dev))
     if code == _lib.SA_ERR_INVALID:  # (every other cause has been checked above)
         _require_apart((k_cache, v_cache, weights, lens),
                        (k_out, v_out, weights_out, lens_out, keep))
-    _lib.check("cache_evict", code)
+    if code:
+        _lib.check("cache_evict", code)
     return k_out, v_out, weights_out, lens_out, keep
 
 
