@@ -98,13 +98,16 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
   int32_t* keep = a.keep + row * a.budget;
   const int n_out = min(n, a.budget);
   const int step = cl * kThreads, first = rank * kThreads + tid;
-  for (int64_t i = n_out + first; i < a.So; i += step) wo[i] = 0.f;
-  for (int i = n_out + first; i < a.budget; i += step) keep[i] = -1;
+  auto fill_tails = [&] {
+    for (int64_t i = n_out + first; i < a.So; i += step) wo[i] = 0.f;
+    for (int i = n_out + first; i < a.budget; i += step) keep[i] = -1;
+  };
   if (n <= a.budget) {  // (the same on every CTA of the cluster)
     for (int i = first; i < n_out; i += step) {
       keep[i] = i;
       wo[i] = __ldg(w + i);
     }
+    fill_tails();
     return;
   }
   const int lo = a.sinks, hi = n - a.recent;         // the candidates
@@ -117,13 +120,22 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
   const int sweeps = KPT > 0 ? KPT : (w1 - w0 + 31) / 32;
   constexpr int kUnroll = KPT > 0 ? KPT : 1;
   constexpr int kHeld = KPT > 0 ? KPT : 1;
+  static_assert(KPT <= 32, "a bit per key");
   uint32_t held[kHeld];
+  uint32_t cand = 0;  // bit j: this lane's key of sweep j is a candidate
   if constexpr (KPT > 0) {
     float x[kHeld];
 #pragma unroll
     for (int j = 0; j < KPT; ++j) x[j] = w0 + 32 * j + lane < w1 ? __ldg(w + w0 + 32 * j + lane) : 0.f;
+    fill_tails();  // (while the loads are on their way)
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) held[j] = weight_key(x[j]);
+    for (int j = 0; j < KPT; ++j) {
+      const int i = w0 + 32 * j + lane;
+      held[j] = weight_key(x[j]);
+      cand |= static_cast<uint32_t>(i < w1 && i >= lo && i < hi) << j;
+    }
+  } else {
+    fill_tails();
   }
   // the key of this lane in sweep j (position w0 + 32 j + lane, below w1)
   auto key_of = [&](int j) -> uint32_t {
@@ -147,21 +159,25 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
       int* const own = hist[pass];
 #pragma unroll(kUnroll)
       for (int j = 0; j < sweeps; ++j) {
-        const int i = w0 + 32 * j + lane;
-        bool count = i < w1 && i >= lo && i < hi;
-        const uint32_t key = count ? key_of(j) : 0u;
-        count = count && (key & fixed) == prefix;
+        bool count;
+        uint32_t key;
+        if constexpr (KPT > 0) {
+          key = held[j];
+          count = ((cand >> j) & 1u) && (key & fixed) == prefix;
+        } else {
+          const int i = w0 + 32 * j + lane;
+          count = i < w1 && i >= lo && i < hi;
+          key = count ? key_of(j) : 0u;
+          count = count && (key & fixed) == prefix;
+        }
         const uint32_t bin = (key >> shift) & digit;
-        // (a warp whose keys all fall into one bin adds once)
-        const uint32_t in = __ballot_sync(0xFFFFFFFFu, count);
-        if (in != 0u) {
-          const int leader = __ffs(in) - 1;
-          const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, bin, leader);
-          if (__all_sync(0xFFFFFFFFu, !count || bin == b0)) {
-            if (lane == leader) atomicAdd(&own[bin], __popc(in));
-          } else if (count) {
-            atomicAdd(&own[bin], 1);
-          }
+        // (a warp whose keys all fall into one bin adds once: 32 adds to one address are taken
+        // one after another)
+        const uint32_t bin0 = __shfl_sync(0xFFFFFFFFu, bin, 0);
+        if (__all_sync(0xFFFFFFFFu, count && bin == bin0)) {
+          if (lane == 0) atomicAdd(&own[bin], 32);
+        } else if (count) {
+          atomicAdd(&own[bin], 1);
         }
       }
       meet();
@@ -203,22 +219,36 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
       need -= pick[1];
     }
   }
-  // `need` of the keys equal to `prefix` stay, the first ones.  Every key's class: kept for
-  // sure (2), equal (1), gone (0).
-  auto class_of = [&](int j) {
+  // `need` of the keys equal to `prefix` stay, the first ones.  Which of this lane's keys are
+  // kept for sure, and which are equal:
+  auto sure_at = [&](int j, bool& equal) {
     const int i = w0 + 32 * j + lane;
-    if (i >= w1) return 0;
-    if (i < lo || i >= hi) return 2;
-    if (chosen == 0) return 0;
+    equal = false;
+    if (i >= w1) return false;
+    if (i < lo || i >= hi) return true;
+    if (chosen == 0) return false;
     const uint32_t key = key_of(j);
-    return key > prefix ? 2 : key == prefix ? 1 : 0;
+    equal = key == prefix;
+    return key > prefix;
   };
+  uint32_t sure = 0, equal = 0;  // as bits (registers)
   int n_in = 0, n_eq = 0;
-#pragma unroll(kUnroll)
-  for (int j = 0; j < sweeps; ++j) {
-    const int c = class_of(j);
-    n_in += __popc(__ballot_sync(0xFFFFFFFFu, c == 2));
-    n_eq += __popc(__ballot_sync(0xFFFFFFFFu, c == 1));
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const bool in = (cand >> j) & 1u;
+      sure |= static_cast<uint32_t>(in ? chosen > 0 && held[j] > prefix : w0 + 32 * j + lane < w1) << j;
+      equal |= static_cast<uint32_t>(in && chosen > 0 && held[j] == prefix) << j;
+    }
+    n_in = __reduce_add_sync(0xFFFFFFFFu, __popc(sure));
+    n_eq = __reduce_add_sync(0xFFFFFFFFu, __popc(equal));
+  } else {
+    for (int j = 0; j < sweeps; ++j) {
+      bool e;
+      const bool in = sure_at(j, e);
+      n_in += __popc(__ballot_sync(0xFFFFFFFFu, in));
+      n_eq += __popc(__ballot_sync(0xFFFFFFFFu, e));
+    }
   }
   if (lane == 0) {
     warp_sum[warp] = n_in;
@@ -244,18 +274,24 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
 #pragma unroll(kUnroll)
   for (int j = 0; j < sweeps; ++j) {
     const int i = w0 + 32 * j + lane;
-    const int c = class_of(j);
-    const uint32_t eq = __ballot_sync(0xFFFFFFFFu, c == 1);
+    bool in, eq;
+    if constexpr (KPT > 0) {
+      in = (sure >> j) & 1u;
+      eq = (equal >> j) & 1u;
+    } else {
+      in = sure_at(j, eq);
+    }
+    const uint32_t ins = __ballot_sync(0xFFFFFFFFu, in);
+    const uint32_t eqs = n_eq > 0 ? __ballot_sync(0xFFFFFFFFu, eq) : 0u;
     // place among the kept: all sure ones and the needed equal ones before it
-    const int eq_at = eq_before + __popc(eq & below);
-    const uint32_t in = __ballot_sync(0xFFFFFFFFu, c == 2);
-    if (c == 2 || (c == 1 && eq_at < need)) {
-      const int at = in_before + __popc(in & below) + min(eq_at, need);
+    const int eq_at = eq_before + __popc(eqs & below);
+    if (in || (eq && eq_at < need)) {
+      const int at = in_before + __popc(ins & below) + min(eq_at, need);
       keep[at] = i;
       wo[at] = __ldg(w + i);  // (its own bits: -0 and every NaN share a key)
     }
-    in_before += __popc(in);
-    eq_before += __popc(eq);
+    in_before += __popc(ins);
+    eq_before += __popc(eqs);
   }
   meet();  // (no CTA leaves while another may read its counts)
 }
