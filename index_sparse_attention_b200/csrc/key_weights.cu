@@ -10,10 +10,10 @@
 // B200 design: one persistent CTA per SM.  The work is a row of units, one 128 x 128 tile of
 // one query head each: key tile after key tile (an item: 128 keys of one (batch, KV head)),
 // inside it the query tiles of its list, inside them the heads of the group (which share the
-// tile's masks).  CTA c of C takes units [U c / C, U (c + 1) / C), so that ragged lists and
-// causal triangles load the SMs evenly.  An item inside one CTA is stored at once; the two ends
-// of a CTA's range can be cut items, whose parts go to the workspace and are added by a second
-// kernel in CTA order.
+// tile's masks).  CTA c takes the units that begin in its share of a line on which units and
+// items' ends are as long as they take, so that ragged lists and causal triangles load the SMs
+// evenly.  An item inside one CTA is stored at once; the two ends of a CTA's range can be cut
+// items, whose parts go to the workspace and are added by a second kernel in CTA order.
 //   warp 0     TMA: an item's K tile and the Q tiles, several stages deep;
 //   warp 1     tcgen05.mma S^T = K Q^T into one of two to four TMEM buffers;
 //   warps 2-17 exp2(S^T scale log2e - lse log2e), summed: thread = key row, a quarter of the
@@ -60,7 +60,7 @@ struct Cfg {
   static constexpr int kDOff = kLOff + kStages * 128 * 4;  // per slot: query tile, list entry
   static constexpr int kXOff = kDOff + 4 * 8;             // part sums, [2][kGroups - 1][128]
   static constexpr int kFindOff = kXOff + 2 * (kGroups - 1) * 128 * 4;
-  static constexpr int kBarOff = kFindOff + 80 * 4;
+  static constexpr int kBarOff = kFindOff + 48 * 8;
   static constexpr int kSmem = kBarOff + 384 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -158,13 +158,24 @@ struct Tiles {
   }
 };
 
-// This CTA's units, the item the first one lies in and the units before that item; called by
-// the whole block, ends with a barrier.
+// The line the work lies on: a unit is kUnit long, and behind an item's units lies kEnd for what
+// its end and the next one's start take.  In hundreds of cycles, measured: with units alone the
+// CTAs with the most items, the short lists of a triangle's last key tiles, took 211 thousand
+// cycles where others took 171 (block-sparse prompt with 32 / 8 heads, S=8192, D=128: 114 us;
+// so 109).
+constexpr int kUnit = 14, kEnd = 28;
+__device__ __forceinline__ int64_t length_of(const Args& a, int64_t n) {
+  return n > 0 ? n * a.G * kUnit + kEnd : 0;
+}
+// This CTA's units: n of them from unit `skip` of item `item` (skip may be the item's number of
+// units: then they begin with the next item's); `at`: where that item begins on the line; q: what
+// a CTA takes of the line, at least a unit, so that every CTA between an item's first and last
+// one holds a part of it.  Called by the whole block, ends with a barrier.
 struct Found {
-  int64_t U, u0, u1, off;
-  int item, C;
+  int64_t at, skip, q;
+  int item, n;
 };
-__device__ __forceinline__ Found find_range(const Args& a, int c, int* sh) {
+__device__ __forceinline__ Found find_range(const Args& a, int c, int64_t* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.items + kThreads - 1) / kThreads;
   const int i0 = min(tid * per, a.items), i1 = min(i0 + per, a.items);
@@ -172,44 +183,75 @@ __device__ __forceinline__ Found find_range(const Args& a, int c, int* sh) {
     return __ldg(a.t.tcnt + 2 * static_cast<int64_t>(i)) +
            __ldg(a.t.tcnt + 2 * static_cast<int64_t>(i) + 1);
   };
-  int mine = 0;
+  int64_t len = 0, num = 0;  // of this thread's items: length, list entries
 #pragma unroll 4
-  for (int i = i0; i < i1; ++i) mine += entries(i);
-  int incl = mine;
+  for (int i = i0; i < i1; ++i) {
+    const int n = entries(i);
+    num += n;
+    len += length_of(a, n);
+  }
+  int64_t incl = len, incl_n = num;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int t = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += t;
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, incl_n, d);
+    if (lane >= d) {
+      incl += x;
+      incl_n += y;
+    }
   }
-  if (lane == 31) sh[warp] = incl;
+  if (lane == 31) {
+    sh[warp] = incl;
+    sh[20 + warp] = incl_n;
+  }
   __syncthreads();
-  int before = 0, total = 0;
+  int64_t before = 0, before_n = 0, U = 0, all_n = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    const int t = sh[w];
-    if (w < warp) before += t;
-    total += t;
+    const int64_t x = sh[w], y = sh[20 + w];
+    if (w < warp) {
+      before += x;
+      before_n += y;
+    }
+    U += x;
+    all_n += y;
   }
-  Found f;
-  f.U = static_cast<int64_t>(total) * a.G;
-  f.C = static_cast<int>(min64(a.C, f.U));
-  f.u0 = c < f.C ? f.U * c / f.C : f.U;
-  f.u1 = c < f.C ? f.U * (c + 1) / f.C : f.U;
-  const int target = static_cast<int>(f.u0 / a.G);  // the entry that the first unit lies in
-  int at = before + incl - mine;
-  if (target >= at && target < at + mine) {
-    for (int i = i0; i < i1; ++i) {
-      const int t = entries(i);
-      if (target < at + t) {
-        sh[64] = i;
-        sh[65] = at;
-        break;
+  Found f{0, 0, 1, 0, 0};
+  if (U == 0) return f;  // (the same on every thread)
+  f.q = max64((U + a.C - 1) / a.C, kUnit);
+  const int64_t x[2] = {min64(U, f.q * c), min64(U, f.q * (c + 1))};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    int64_t at = before + incl - len, at_n = before_n + incl_n - num;
+    if (x[e] < U && x[e] >= at && x[e] < at + len) {
+      for (int i = i0; i < i1; ++i) {
+        const int n = entries(i);
+        const int64_t l = length_of(a, n);
+        if (x[e] < at + l) {
+          sh[40 + 4 * e] = i;
+          sh[41 + 4 * e] = at;
+          sh[42 + 4 * e] = at_n;
+          sh[43 + 4 * e] = n;
+          break;
+        }
+        at += l;
+        at_n += n;
       }
-      at += t;
     }
   }
   __syncthreads();
-  f.item = f.u0 < f.u1 ? sh[64] : 0;
-  f.off = f.u0 < f.u1 ? static_cast<int64_t>(sh[65]) * a.G : 0;
+  int64_t done[2];  // units before x[0] and x[1]
+#pragma unroll
+  for (int e = 1; e >= 0; --e) {
+    if (x[e] >= U) {
+      done[e] = all_n * a.G;
+      continue;
+    }
+    f.item = static_cast<int>(sh[40 + 4 * e]);
+    f.at = sh[41 + 4 * e];
+    f.skip = min64(sh[43 + 4 * e] * a.G, (x[e] - f.at + kUnit - 1) / kUnit);
+    done[e] = sh[42 + 4 * e] * a.G + f.skip;
+  }
+  f.n = static_cast<int>(done[1] - done[0]);
   return f;
 }
 
@@ -243,13 +285,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Found f = find_range(ka, cta, reinterpret_cast<int*>(smem + C::kFindOff));
+  const Found f = find_range(ka, cta, reinterpret_cast<int64_t*>(smem + C::kFindOff));
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  const int n_iter = __shfl_sync(0xFFFFFFFFu, static_cast<int>(f.u1 - f.u0), 0);
+  const int n_iter = __shfl_sync(0xFFFFFFFFu, f.n, 0);
   if (n_iter == 0 && threadIdx.x == 0) ka.fix[cta] = make_int2(-1, 0);
   Part p{};
-  if (n_iter > 0) p.open(ka, f.item, f.u0 - f.off, n_iter);
+  if (n_iter > 0) {
+    p.open(ka, f.item, f.skip, n_iter);
+    if (p.units == 0) p.next(ka, n_iter);
+  }
   int issued_q = 0, issued_k = 0;
 
   if (warp == 0) {
@@ -395,10 +440,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t cm = 0u;  // which of the tile's queries [32 wg, 32 wg + 32) see this key
     bool ok = true, cut_here = false;
     int part = 0, it = 0;
-    int64_t start = f.off;  // first unit of the item
+    int64_t at = f.at;       // where the item begins on the line
+    int64_t skip = f.skip;   // units of the item before this CTA's
+    if (n_iter > 0 && p.item != f.item) {
+      at += length_of(ka, __ldg(a.tcnt + 2 * static_cast<int64_t>(f.item)) +
+                              __ldg(a.tcnt + 2 * static_cast<int64_t>(f.item) + 1));
+      skip = 0;
+    }
     while (it < n_iter) {
       // ------------------------------------------------------------ one part: units of an item
-      const int64_t end = start + static_cast<int64_t>(p.n) * ka.G;
+      const int64_t all = static_cast<int64_t>(p.n) * ka.G;
       const int it_end = it + p.units;
       const int item = p.item, n_full = p.n_full, nt = p.nt, bg = p.item / a.Tn;
       const int64_t j = static_cast<int64_t>(nt) * 128 + r;
@@ -478,22 +529,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wg == 0) {
 #pragma unroll
         for (int x = 0; x < kGroups - 1; ++x) total += xp[x * 128 + r];
-        const bool begins = start >= f.u0, ends = end <= f.u1;
+        const bool begins = skip == 0, ends = skip + p.units == all;
         if (begins && ends) {
           if (key_ok) {
-            const int64_t at = static_cast<int64_t>(bg) * a.Sk + j;
-            ka.w_out[at] = ka.w_in ? ka.w_in[at] + total : total;
+            const int64_t to = static_cast<int64_t>(bg) * a.Sk + j;
+            ka.w_out[to] = ka.w_in ? ka.w_in[to] + total : total;
           }
         } else if (begins) {
           ka.tail[cta * 128 + r] = total;
           cut_here = true;
           if (r == 0)
-            ka.fix[cta] = make_int2(item, static_cast<int>((end * f.C - 1) / f.U));
+            ka.fix[cta] = make_int2(item, static_cast<int>((at + (all - 1) * kUnit) / f.q));
         } else {
           ka.head[cta * 128 + r] = total;
         }
       }
-      start = end;
+      at += length_of(ka, p.n);
+      skip = 0;
       ++part;
       if (it < n_iter) p.next(ka, n_iter - it);
     }
