@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(352, 1)
     // ---------------------------------------------------------------- Q and K producer
     if (cta == 0)  // lengths out of range are reported once
       for (int b = lane; b < a.B; b += 32) {
-        const int n = __ldg(a.lens + b);
+        const int n = ld_behind(a.lens + b);
         if (n < 0 || n > a.S) report_status(a.status, kStatusIndex);
       }
     bool first = true, was_full = false;
@@ -516,11 +516,9 @@ __global__ void __launch_bounds__(352, 1)
 // join: kW warps per (sequence, query head) row, 4 / kW rows per block.  Every warp finds the
 // parts' common maximum and sum (one part per lane), then takes every kW-th part's output, four
 // loads in flight.  Few rows have many parts (up to one per CTA) and take four warps each; from
-// kJoinRows rows on the blocks are many and the parts few, and a warp does a row (8192 rows of
-// two or three parts: 36 us with four warps, 17 with one).
+// kJoinRows rows on the blocks are many and the parts few, and a warp does a row.
 // ------------------------------------------------------------------------------------
 constexpr int kJoin = 128;
-constexpr int kJoinRows = 2048;
 
 template <int DV, int kW>
 __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
@@ -532,17 +530,24 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   if (row >= static_cast<int64_t>(a.B) * a.HQ) return;  // (kW == 1 only: a whole warp)
   const int b = static_cast<int>(row / a.HQ), h = static_cast<int>(row - static_cast<int64_t>(b) * a.HQ);
   const int hk = h / a.G, g = h - hk * a.G;
-  // the plan's line up to this sequence and in all (every warp for itself)
+  // the plan's line up to this sequence and in all
   int64_t before = 0, total = 0;
-  for (int x = lane; x < a.B; x += 32) {
-    const int64_t t = length_of(a, tiles_of(a, clamped_len(a, x)), a.wt_c);
-    total += t;
-    if (x < b) before += t;
-  }
+  const bool summed = kW == 1 && a.line;
+  if (summed) {
+    wait_previous_kernel();
+    before = a.line[b];
+    total = a.line[a.B];
+  } else {
+    for (int x = lane; x < a.B; x += 32) {
+      const int64_t t = length_of(a, tiles_of(a, clamped_len(a, x)), a.wt_c);
+      total += t;
+      if (x < b) before += t;
+    }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
-    total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    for (int d = 16; d; d >>= 1) {
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
+      total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    }
   }
   const int64_t np = prefix_length(a), U = np + total * a.HK;
   const int64_t q = share_of(a, U);
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
     return i < n_p ? a.po_p + (at_p + static_cast<int64_t>(i) * a.rows_p) * DV
                    : a.po_c + (at_c + static_cast<int64_t>(i - n_p) * a.rows_c) * DV;
   };
-  wait_previous_kernel();
+  if (!summed) wait_previous_kernel();
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, ml_of(i)->x);
 #pragma unroll
@@ -739,6 +744,9 @@ static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
   a->po_p = reinterpret_cast<float*>(take(parts_p * p->Dv * sizeof(float)));
   a->ml_c = reinterpret_cast<float2*>(take(parts_c * sizeof(float2)));
   a->po_c = reinterpret_cast<float*>(take(parts_c * p->Dv * sizeof(float)));
+  a->line = nullptr;
+  if (p->B >= kLineSeqs && static_cast<int64_t>(p->B) * p->HQ >= kJoinRows)
+    a->line = reinterpret_cast<int64_t*>(take((static_cast<size_t>(p->B) + 1) * sizeof(int64_t)));
   a->scores = nullptr;
   if (p->weights_out)
     a->scores = reinterpret_cast<float*>(

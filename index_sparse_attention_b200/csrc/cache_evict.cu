@@ -7,15 +7,15 @@
 //              in registers as order-preserving keys (4, 8 or 16 per thread; longer slices are
 //              read again in every sweep).  Radix select of the smallest kept weight in three
 //              digit passes (11, 11, 10 bits): each CTA counts its keys in shared memory and adds
-//              up a share of the bins over the cluster (distributed shared memory) for all.  Then every warp counts its stretch of the
-//              row by ballots, one scan over the warps and CTAs gives each its place, and a last
-//              sweep writes the positions in order: keys above the threshold, and of those equal
-//              to it the first ones that are still needed.  The sweeps are bound by their
-//              instructions (with the slice in shared memory and 64-bit positions: 39 us for 32
-//              rows of 65536; with registers xx).
+//              up a share of the bins over the cluster (distributed shared memory) for all.
+//              Then every warp counts its stretch of the row, one scan over the warps and CTAs
+//              gives each its place, and a last sweep writes the positions in order: keys above
+//              the threshold, and of those equal to it the first ones that are still needed.
+//              Bound by the sweeps' instructions and the cluster's meetings, not by bytes: 24 us
+//              for 32 rows of 65536 (with the slice in shared memory and 64-bit positions 39).
 //   copy       16-byte pieces, four rows per thread in flight, writes contiguous over all heads
-//              of a row.
-// The copy is bound by HBM (each kept row is read and written once).
+//              of a row.  Bound by HBM (each kept row is read and written once): 16 sequences of
+//              8 heads cut from 8191 to 2048 keys, D=128, 56 us in all, 4.7 TB/s of its bytes.
 #include "sa_device.cuh"
 #include "sa_kernels.h"
 
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
   const int b = static_cast<int>(row / a.HK), hk = static_cast<int>(row - static_cast<int64_t>(b) * a.HK);
   wait_previous_kernel();
   allow_next_kernel();
-  const int raw = __ldg(a.lens + b);
+  const int raw = ld_behind(a.lens + b);  // (every other load depends on it)
   const int n = static_cast<int>(min64(max64(static_cast<int64_t>(raw), 0), a.S));
   if (tid == 0 && hk == 0 && rank == 0) {
     if (raw != n) report_status(a.status, kStatusIndex);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const Args a) {
 // quotient for each, the large copies took half as long again).
 template <int kN>
 __device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* __restrict__ dst,
-                                          const int32_t* __restrict__ keep, int budget, int HK,
+                                          const int32_t* keep, int budget, int HK,
                                           int per_head, int i0, int rows) {
   const int per_row = HK * per_head;
   for (int p = threadIdx.x; p < per_row; p += 256) {
@@ -311,7 +311,7 @@ __device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* 
       uint4 x[kN];
 #pragma unroll
       for (int e = 0; e < kN; ++e)
-        if (r + e < rows) from[e] = __ldg(kp + r + e);
+        if (r + e < rows) from[e] = kp[r + e];
 #pragma unroll
       for (int e = 0; e < kN; ++e)
         if (r + e < rows) x[e] = __ldg(src + from[e] * per_row + p);
@@ -324,7 +324,7 @@ __device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* 
 __global__ void __launch_bounds__(256) evict_copy_kernel(const Args a) {
   const int b = blockIdx.y;
   wait_previous_kernel();
-  const int n_out = static_cast<int>(min64(max64(static_cast<int64_t>(__ldg(a.lens + b)), 0),
+  const int n_out = static_cast<int>(min64(max64(static_cast<int64_t>(ld_behind(a.lens + b)), 0),
                                            min64(a.S, a.budget)));
   const int i0 = blockIdx.x * a.rows, rows = min(a.rows, n_out - i0);
   if (rows <= 0) return;

@@ -24,6 +24,14 @@ namespace sa {
 namespace cache {
 
 constexpr int kMaxCtas = 256;  // bound of C the workspace is sized for
+// From so many (sequence, query head) rows on the join gives a row one warp instead of four
+// (8192 rows of two or three parts: 36 us with four warps, 17 with one).
+constexpr int kJoinRows = 2048;
+// From so many sequences on such a join takes their places on the line from the workspace; with
+// fewer each warp adds up the lengths itself while the parts are computed (32 heads, D=128, the
+// whole call: 128 sequences of 1024 keys 93.8 us from the workspace, 92.5 without; 256 with a
+// prefix of 8192 92.3 and 93.2; 1024 of 256 keys 200 and 232; 4096 of 128 keys 623 and 1167).
+constexpr int kLineSeqs = 256;
 
 struct Args {
   const __nv_bfloat16 *q, *k, *v, *kp, *vp;
@@ -37,6 +45,7 @@ struct Args {
   float2 *ml_p, *ml_c;
   float *po_p, *po_c;
   float* scores;
+  int64_t* line;  // [B + 1] the lengths before each sequence, for one KV head, and of all; or null
   int B, HQ, HK, G, Dqk, Dv;
   int64_t S, P, Sp;  // Sp: row stride of scores
   int kshift;        // log2 of the keys of a tile
@@ -53,7 +62,7 @@ struct Args {
 };
 
 __device__ __forceinline__ int64_t clamped_len(const Args& a, int b) {
-  return min64(max64(static_cast<int64_t>(__ldg(a.lens + b)), 0), a.S);
+  return min64(max64(static_cast<int64_t>(ld_behind(a.lens + b)), 0), a.S);
 }
 __device__ __forceinline__ int64_t tiles_of(const Args& a, int64_t len) {
   return (len + (1 << a.kshift) - 1) >> a.kshift;
@@ -123,6 +132,14 @@ __device__ __forceinline__ Found find_range(const Args& a, int c, int64_t* sh) {
     }
     total += x;
     total_t += y;
+  }
+  if (c == 0 && a.line) {
+    int64_t at = before + incl - len;
+    for (int b = b0; b < b1; ++b) {
+      a.line[b] = at;
+      at += length_of(a, tiles_of(a, clamped_len(a, b)), a.wt_c);
+    }
+    if (tid == 0) a.line[a.B] = total;
   }
   const int64_t np = prefix_length(a), U = np + total * a.HK;
   Found f{0, 0, -1, 0};

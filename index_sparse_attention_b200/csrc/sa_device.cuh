@@ -412,6 +412,18 @@ __device__ __forceinline__ void tmem_wait_st() {
 __device__ __forceinline__ void wait_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// Loads of what the kernel before may write: unlike __ldg they cannot be moved ahead of that
+// wait, and unlike plain loads they need not wait for the stores between them.
+__device__ __forceinline__ float ld_behind(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_behind(const int* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ void allow_next_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

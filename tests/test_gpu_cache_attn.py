@@ -91,6 +91,9 @@ CASES = {
     "many_rows_d256": dict(lens=[5 + 3 * i for i in range(40)], HQ=8, HK=1, D=D256, P=260),
     "many_sequences": dict(lens=[(7 * i) % 50 for i in range(400)], HQ=2, HK=1, D=D64, P=33),
     "more_sequences_than_threads": dict(lens=[(i % 3) for i in range(1500)], HQ=1, HK=1, D=D64),
+    "many_sequences_and_rows": dict(lens=[(37 * i) % 190 for i in range(300)], HQ=8, HK=2, D=D128,
+                                    P=140),
+    "many_rows_no_prefix_d192": dict(lens=[(i % 7) * 21 for i in range(520)], HQ=4, HK=4, D=D192),
     "sharp": dict(lens=[500, 333], HQ=8, HK=2, D=D128, P=300, kscale=12.0),
 }
 
