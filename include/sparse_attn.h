@@ -349,7 +349,8 @@ int topk_select(const float *scores, int64_t rows, int64_t cols, int64_t ld,
  * Serving from a cache: attention of one new token per sequence over a prefix that the
  * whole batch shares and each sequence's own cache, the attention weight the cached keys
  * have received, and eviction by that weight.  (The pages have no counterpart; layouts,
- * head dims and error rules are those above.)
+ * head dims and error rules are those above.)  These calls launch kernels only: they can be
+ * captured into CUDA graphs, which read the lengths anew at every replay.
  * ------------------------------------------------------------------------------------ */
 typedef struct cache_attn_params {
   const void *q;                  /* bf16 [B][1][HQ][Dqk]: one query token per sequence */
@@ -379,7 +380,7 @@ typedef struct cache_attn_params {
  * the call.  Rows of the caches behind lens[b] are never used, whatever they hold.  A
  * sequence with no key at all (lens[b] == 0, P == 0) gets o = 0, lse = -inf.  A length
  * outside [0, S] is clamped to that range and sets SA_STATUS_INDEX in *dev_status.
- * Supported: HQ / HK <= 128 (SA_ERR_UNSUPPORTED above).  `workspace` is device memory of at
+ * Supported: HQ / HK <= 128, B and HQ <= 65535 (SA_ERR_UNSUPPORTED above).  `workspace` is device memory of at
  * least cache_attn_workspace_size() bytes, 16-byte aligned, not initialised, used by this
  * call alone until its work has run.  Results do not depend on the order in which CTAs run.
  */
@@ -400,7 +401,7 @@ size_t cache_attn_workspace_size(const cache_attn_params *p);
  *   weights, weights_out  fp32 [B][HK][Sk]; may be the same array.
  * The sums are taken in a fixed order (two calls give identical bits).  `workspace`: device
  * memory of at least sparse_attn_key_weights_workspace_size() bytes,
- * 16-byte aligned, not initialised.
+ * 16-byte aligned, not initialised, used by this call alone until its work has run.
  */
 int sparse_attn_key_weights(const sparse_attn_params *p, const float *weights,
                             float *weights_out, void *workspace, size_t workspace_bytes,
@@ -434,7 +435,8 @@ typedef struct cache_evict_params {
  *   lens_out[b]      min(lens[b], budget).
  * No output may overlap an input or another output (SA_ERR_INVALID).
  * 1 <= budget <= S_out, sinks, recent >= 0, sinks + recent <= budget.  A length outside
- * [0, S] is clamped and sets SA_STATUS_INDEX in *dev_status.  Needs no workspace.
+ * [0, S] is clamped and sets SA_STATUS_INDEX in *dev_status.  B and HK <= 65535.  Needs no
+ * workspace.
  */
 int cache_evict(const cache_evict_params *p, sa_stream_t stream);
 

@@ -144,6 +144,46 @@ def test_graph_replay_with_other_contents():
     _check(k, v, w, lens, out, 300, 4, 32)
 
 
+def test_two_calls_at_once_on_two_streams():
+    import torch
+    import index_sparse_attention_b200 as sa
+    cases = [_make([20000, 9000, 1], 2, D128, 20000, 71), _make([3000, 2999, 3000], 2, D64, 3000, 72)]
+    torch.cuda.synchronize()
+    streams, out = [torch.cuda.Stream() for _ in cases], [None, None]
+    for _ in range(3):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                out[i] = sa.cache_evict(*c[4], 300, sinks=4, recent=32)
+    torch.cuda.synchronize()
+    for c, got in zip(cases, out):
+        _check(*c[:4], got, 300, 4, 32)
+
+
+def test_offsets_beyond_32_bits():
+    """Caches of 2^32 elements: the rows of the last sequence are found at their far end."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    B, S, HK, D, budget = 2, 1 << 22, 4, 128, 200
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    k = torch.empty((B, S, HK, D), dtype=torch.bfloat16, device="cuda")
+    k.view(torch.int16)[:] = torch.arange(S, device="cuda").to(torch.int16)[None, :, None, None]
+    w = torch.rand((B, HK, S), device="cuda")
+    w[1, :, -1000:] += 1.0  # (more of the largest than are kept)
+    lens = torch.tensor([7, S], dtype=torch.int32, device="cuda")
+    ko = torch.zeros((B, budget, HK, D), dtype=torch.bfloat16, device="cuda")
+    ko, vo, wo, lo, keep = sa.cache_evict(k, k, w, lens, budget, k_out=ko)
+    assert lo.tolist() == [7, budget]
+    for h in range(HK):
+        at = torch.argsort(w[1, h, -1000:], descending=True, stable=True)[:budget] + (S - 1000)
+        at = at.sort().values
+        assert torch.equal(keep[1, h].long(), at)
+        assert torch.equal(wo[1, h], w[1, h, at])
+        assert torch.equal(ko[1, :, h].view(torch.int16), k[1, at, h].view(torch.int16))
+        assert torch.equal(vo[1, :, h].view(torch.int16), k[1, at, h].view(torch.int16))
+
+
 def test_overlapping_outputs_are_refused():
     import torch
     import index_sparse_attention_b200 as sa

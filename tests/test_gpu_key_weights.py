@@ -41,6 +41,11 @@ CASES = [
              name="many_tiles_d256"),
     I.scaled(IDX, Sq=1401, Sk=1401, HQ=32, HK=4, Dqk=128, topk=200, name="index_many_tiles_d128"),
     I.scaled(IDX, Sq=1401, Sk=1401, HQ=32, HK=4, topk=200, name="index_many_tiles_d192"),
+    # many key tiles of one query tile each, or of none
+    I.scaled(GQA, B=4, Sq=100, Sk=1500, HQ=8, HK=8, causal=False, density=1.0, name="short_lists"),
+    I.scaled(GQA, B=2, Sq=130, Sk=3001, HQ=4, HK=4, causal=False, density=0.2, name="empty_lists"),
+    I.scaled(GQA, B=2, Sq=257, Sk=6000, HQ=5, HK=5, Dqk=256, Dv=256, causal=False, density=0.5,
+             name="short_lists_d256"),
 ]
 
 
@@ -141,3 +146,59 @@ def test_short_wait_limit_reports_timeout_then_recovers(w):
     status.zero_()
     again = sa.sparse_attn_key_weights(g["q"], g["k"], lse, bsp, w.scale, dev_status=status)
     assert int(status.item()) == 0 and torch.equal(again, got)
+
+
+def test_other_stream_and_graph_replay():
+    import torch
+    import index_sparse_attention_b200 as sa
+    g, bsp, lse, got, ref, tol = _run(CASES[3])
+    q, k = g["q"], g["k"]
+    side = torch.cuda.Stream()
+    out = torch.full_like(got, float("nan"))
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sa.sparse_attn_key_weights(q, k, lse, bsp, CASES[3].scale, weights_out=out)
+    side.synchronize()
+    assert torch.equal(out, got)
+    qs, ls = torch.zeros_like(q), torch.zeros_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.sparse_attn_key_weights(qs, k, ls, bsp, CASES[3].scale, weights_out=out)
+    for _ in range(2):
+        qs.copy_(q)
+        ls.copy_(lse)
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got)
+
+
+def test_offsets_beyond_32_bits():
+    """Q of 2^32 elements: the last query tile of the second batch is found."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    B, Sq, HQ, HK, D, Sk = 2, 1 << 18, 32, 4, 256, 200
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    rng = np.random.default_rng(5)
+    q = torch.zeros((B, Sq, HQ, D), dtype=torch.bfloat16, device="cuda")
+    rows = [*range(64), *range(Sq - 128, Sq)]
+    few = torch.from_numpy(rng.standard_normal((B, len(rows), HQ, D)).astype(np.float32))
+    q[:, rows] = few.bfloat16().cuda()
+    k = torch.from_numpy(rng.standard_normal((B, Sk, HK, D)).astype(np.float32)).bfloat16().cuda()
+    mask = np.zeros((B, HK, Sq // 128, 2), np.uint8)
+    mask[:, :, 0, 0] = mask[:, :, -1] = 1
+    bsp = sa.block_mask_to_block_sparse(torch.from_numpy(mask).cuda(), B, HK, Sq, Sk, bs=128)
+    rows = [*range(128), *range(Sq - 128, Sq)]
+    allowed = np.zeros((B, HK, 256, Sk), bool)
+    allowed[:, :, :128, :128] = allowed[:, :, 128:] = True
+    qr = q[:, rows].double().unflatten(2, (HK, -1))
+    s = torch.einsum("bqghd,bkgd->bghqk", qr, k.double()) * D ** -0.5
+    s = s.masked_fill(~torch.from_numpy(allowed).cuda()[:, :, None], float("-inf"))
+    lse = torch.full((B, HQ, Sq), float("-inf"), device="cuda")
+    lse[:, :, rows] = s.logsumexp(-1).flatten(1, 2).float()
+    got = sa.sparse_attn_key_weights(q, k, lse, bsp)
+    ref, tol = R.key_weights(bf16_to_f64(q[:, rows].contiguous()), bf16_to_f64(k),
+                             lse[:, :, rows].double().cpu().numpy(), allowed, D ** -0.5)
+    _compare(got, ref, tol)
