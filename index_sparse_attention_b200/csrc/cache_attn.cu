@@ -190,8 +190,6 @@ __global__ void __launch_bounds__(352, 1)
       if (first_s && !warp_wait(BAR(kBQF + qs), qu & 1, ctl, a.status, a.wait_limit_ns)) return false;
       if (!warp_wait(BAR(kBKF + ks), ku & 1, ctl, a.status, a.wait_limit_ns)) return false;
       tc_fence_after();
-      const bool more = it + 1 < n_iter;
-      const bool ends = !more || w.next(a);  // the part's last tile
       const uint64_t kd = sw128_desc(sbase + C::kKOff + ks * C::kKBytes, 16, 1024);
       const uint64_t qd = sw128_desc(sbase + (C::kQBufs == 2 ? qs * C::kQBytes : 0), 16, 1024);
       if (elect_one()) {
@@ -201,9 +199,13 @@ __global__ void __launch_bounds__(352, 1)
                   kd + (((kk >> 2) * C::kKPanel + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
         umma_commit(BAR(kBSF + (it & 1)));
         umma_commit(BAR(kBKE + ks));
-        if (ends) umma_commit(BAR(kBQE + qs));
       }
       __syncwarp();
+      const bool ends = it + 1 >= n_iter || w.next(a);  // the part's last tile
+      if (ends) {
+        if (elect_one()) umma_commit(BAR(kBQE + qs));
+        __syncwarp();
+      }
       first_s = ends;
       if (ends) ++part;
       return true;
@@ -215,8 +217,9 @@ __global__ void __launch_bounds__(352, 1)
       const bool last = first_s;
       if (!last && it + 1 < n_iter && !issue_s(it + 1)) break;
       const int vs = it % C::kVStages, vu = it / C::kVStages;
-      if (!warp_wait(BAR(kBPF + (it & 1)), (it >> 1) & 1, ctl, a.status, a.wait_limit_ns)) break;
+      // (V first: it has long come when P has, and a wait costs 150 cycles)
       if (!warp_wait(BAR(kBVF + vs), vu & 1, ctl, a.status, a.wait_limit_ns)) break;
+      if (!warp_wait(BAR(kBPF + (it & 1)), (it >> 1) & 1, ctl, a.status, a.wait_limit_ns)) break;
       tc_fence_after();
       const uint64_t vd = sw128_desc(sbase + C::kVOff + vs * C::kVBytes, C::kKPanel, 1024);
       if (elect_one()) {
@@ -252,9 +255,8 @@ __global__ void __launch_bounds__(352, 1)
       const int c0 = rep ? quarter * (kN / 4) + hc * NC : hc * NC;
       const int k0 = static_cast<int>(w.tile) * kN;
       const int lim = static_cast<int>(min64(kN, w.keys - k0));
-      if (!both(__all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBSF + sb), (it >> 1) & 1, ctl, a.status,
-                                                  a.wait_limit_ns))))
-        return false;
+      const bool there = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBSF + sb), (it >> 1) & 1, ctl,
+                                                           a.status, a.wait_limit_ns));
       tc_fence_after();
       uint32_t u[NC];
       if constexpr (NC >= 32) {
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(352, 1)
           if (c0 + c >= lim) x[c] = -INFINITY;
       }
       const float sc = a.scale_log2;
-      if (a.scores && !w.prefix && active) {
+      if (a.scores && !w.prefix && active && there) {
         const int g = rep ? lane - loff : r;
         float4* dst = reinterpret_cast<float4*>(
             a.scores + (static_cast<int64_t>(w.b) * a.HQ + w.hk * a.G + g) * a.Sp + k0 + c0);
@@ -297,7 +299,8 @@ __global__ void __launch_bounds__(352, 1)
       float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * sc;
       xch[hc * 128 + r] = mx;
       // both warps have read their S columns past this barrier: P may be written over them
-      named_bar_sync(pair_bar, 64);
+      // (one whose wait gave up has read what was there, and both leave)
+      if (!both(there)) return false;
       mx = fmaxf(xch[r], xch[128 + r]);
       const bool need = active && mx > m_run + 8.0f;
       const float alpha = need ? ex2(m_run - mx) : 1.f;
