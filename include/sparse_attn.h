@@ -380,9 +380,10 @@ typedef struct cache_attn_params {
  * the call.  Rows of the caches behind lens[b] are never used, whatever they hold.  A
  * sequence with no key at all (lens[b] == 0, P == 0) gets o = 0, lse = -inf.  A length
  * outside [0, S] is clamped to that range and sets SA_STATUS_INDEX in *dev_status.
- * Supported: HQ / HK <= 128, B and HQ <= 65535 (SA_ERR_UNSUPPORTED above).  `workspace` is device memory of at
- * least cache_attn_workspace_size() bytes, 16-byte aligned, not initialised, used by this
- * call alone until its work has run.  Results do not depend on the order in which CTAs run.
+ * Supported: HQ / HK <= 128, B and HQ <= 65535 (SA_ERR_UNSUPPORTED above).  `workspace` is
+ * device memory of at least cache_attn_workspace_size() bytes, 16-byte aligned, not
+ * initialised, used by this call alone until its work has run.  Results do not depend on the
+ * order in which CTAs run.
  */
 int cache_attn_fwd(const cache_attn_params *p, void *workspace, size_t workspace_bytes,
                    sa_stream_t stream);

@@ -5,8 +5,32 @@
 // over a run of keys holds m = max s_j, l = sum exp(s_j - m), o = sum exp(s_j - m) v_j; parts
 // join as m' = max m, l' = sum l exp(m - m'), o' = sum o exp(m - m') (fp32 throughout), and
 // lse = m' + ln l', o = o' / l'.
-// Three launches: the parts (this file's main kernel, work split as in cache_plan.cuh), their
-// join, and, when asked for, the keys' weights from the stored scores.
+//
+// B200 design: three launches, each started while the one before it ends (programmatic dependent
+// launch): the parts, their join, and, when asked for, the keys' weights from the stored scores.
+// The parts kernel is one persistent CTA per SM over an even share of all key tiles
+// (cache_plan.cuh), so that one long sequence, a ragged batch and a long prefix all fill the GPU:
+//   warp 0     TMA: Q rows of a part, K tiles (two to five stages); warp 10: V tiles;
+//   warp 1     tcgen05.mma: S = Q K^T into one of two TMEM buffers, O += P V with P read from TMEM;
+//              S of the next tile is issued before P V of this one;
+//   warps 2-9  softmax, two warps per TMEM lane quarter: scores, running maximum and sum, P (bf16)
+//              over S, the part's end.
+// A prefix part holds the query rows of up to 128 / group sequences (box {64, sequences, group} of
+// one TMA load), so a prefix tile is read once for all of them; a cache part holds the group's
+// rows.  An MMA has 128 rows: parts of up to 32 rows load their Q into all four lane quarters, and
+// each quarter's copy takes a quarter of the tile's keys (P is 0 elsewhere), so that all eight
+// softmax warps share the exponentials; the copies are added when the part ends.
+// P is rounded to bf16 for the MMA, as the forward does (its sum is taken before in fp32).  The
+// running maximum moves only when a row's exceeds it by 8 (factors up to 2^8 in P, O and l).
+// What bounds it: HBM where the caches are long (64 sequences of 4096 keys, 8 KV heads, D=128:
+// 165 us, 6.5 TB/s, the copy bandwidth measured on this GPU); the softmax warps' chain on prefix
+// tiles of many rows (2250 cycles per 128 x 128 tile, of which the exponentials 1200 and the MMAs
+// 1050: 256 sequences over a prefix of 8192, 92 us, 375 TFLOP/s); on short calls the launches,
+// the set-up (lengths, plan, first loads: about 5 us) and the join (3 us).
+// Tried without gain: a third K stage; both softmax groups with a tile and an O of their own by
+// turns (2250 cycles a tile again: then the MMA warp's waits and issues bound); an eighth to a
+// half of the exponentials by polynomial (2% on prefix tiles); joining and weighing in one launch
+// (1.5 to 3 us slower).
 #include <type_traits>
 
 #include "cache_plan.cuh"
@@ -645,7 +669,9 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
 }
 
 // ------------------------------------------------------------------------------------
-// weights: one thread per key of a (sequence, KV head)
+// weights: one thread per key of a (sequence, KV head) sums the group's probabilities from the
+// scores that the parts kernel stored (fp32, log2 units) and the joined lse.  A few microseconds,
+// launch-bound: 16 sequences of 2049 keys, 32 heads, read 4 MB that the L2 holds.
 // ------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) cache_weights_kernel(const Args a) {
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;

@@ -9,10 +9,10 @@
 // the lengths are, and a segment that crosses a border is cut there.  (Counting tiles alone left
 // the CTA with the shortest sequences behind: 12 segments of one tile in its 15 tiles, 75000
 // cycles against 43000.)  q is at least the longer tile: then every CTA between a segment's
-// first and last one holds a part of it.  A part (segment s, CTA c) writes its un-normalised output and its
-// running max and sum to slot s + c: along the line each part has a larger s or a larger c than
-// the one before, so no two share a slot, and the joining kernel finds a segment's parts from
-// the same arithmetic.
+// first and last one holds a part of it.  A part (segment s, CTA c) writes its un-normalised
+// output and its running max and sum to slot s + c: along the line each part has a larger s or a
+// larger c than the one before, so no two share a slot, and the joining kernel finds a segment's
+// parts from the same arithmetic.
 #pragma once
 
 #include <cuda_bf16.h>
