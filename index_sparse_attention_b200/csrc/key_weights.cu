@@ -23,13 +23,14 @@
 //              lose low bits.
 //   warp 18    feeds the units' lse values and list entries through shared memory.
 // What bounds it: the special-function unit.  A unit's 16384 exponentials take an SM 1024 cycles
-// (its MMAs 512 at head dim 128); measured 1360 cycles a unit on long prompts (107 us for the
-// causal prompt B=2 H=16 S=4096 D=128, 642 TFLOP/s of allowed pairs; 116 us for the index prompt
-// with 32 heads, S=4001, head dims 192/128).  Tried and slower: a unit per warpgroup (113 us;
-// a group stands idle while its buffer is refilled), eight warps with half a unit each and the
-// next half's TMEM loads in flight (130 us; the remaining latency of a unit is shared by fewer
-// warps), an eighth to a half of the exponentials by a polynomial of packed fused multiply-adds
-// (107 to 124 us: the warps are short of issue slots, not of that unit alone).
+// (its MMAs 512 at head dim 128); measured 1300 to 1400 cycles a unit on long prompts (101 us for
+// the causal prompt B=2 H=16 S=4096 D=128, 679 TFLOP/s of allowed pairs; 104 us for the
+// block-sparse one with 32 / 8 heads, S=8192; 113 us for the index prompt with 32 / 4 heads,
+// S=4001, head dims 192/128).  Tried and slower: a unit per warpgroup (a group stands idle while
+// its buffer is refilled), eight warps with half a unit each and the next half's TMEM loads in
+// flight (the remaining latency of a unit is shared by fewer warps), an eighth to a half of the
+// exponentials by a polynomial of packed fused multiply-adds (equal to slower: the warps are
+// short of issue slots and latency, not of that unit alone).
 // Every mbarrier wait is bounded (sa_device.cuh).
 #include <type_traits>
 
@@ -494,23 +495,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const ulonglong2* ls2 = reinterpret_cast<const ulonglong2*>(lse_s + st * 128 + 32 * wg);
-        uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};  // pairs of sums
+        uint64_t ps[2] = {0ull, 0ull};  // pairs of sums
         tmem_wait_ld();
+        // Masked tiles: packed multiply-adds, and only what the key sees is added; the others:
+        // scalar multiply-adds and packed sums (measured so: the compiler's schedules of the
+        // four combinations differ by up to 6%).
         auto sweep = [&](auto masked) {
           constexpr bool kMasked = decltype(masked)::value;
+          float seen[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const ulonglong2 l = ls2[e >> 1];
-            const uint64_t t2 = fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
-                                     pack2(sc, sc), (e & 1) ? l.y : l.x);
-            const float2 t = unpack2(t2);
-            float p0 = ex2(t.x), p1 = ex2(t.y);
+            const float s0 = __uint_as_float(s[2 * e]), s1 = __uint_as_float(s[2 * e + 1]);
+            const uint64_t l = (e & 1) ? ls2[e >> 1].y : ls2[e >> 1].x;
             if constexpr (kMasked) {
-              p0 = (cm >> (2 * e)) & 1u ? p0 : 0.f;
-              p1 = (cm >> (2 * e + 1)) & 1u ? p1 : 0.f;
+              const float2 t = unpack2(fma2(pack2(s0, s1), pack2(sc, sc), l));
+              const float p0 = ex2(t.x), p1 = ex2(t.y);
+              if (cm & (1u << (2 * e))) seen[(2 * e) & 3] += p0;
+              if (cm & (2u << (2 * e))) seen[(2 * e + 1) & 3] += p1;
+            } else {
+              const float2 lv = unpack2(l);
+              const float p0 = ex2(fmaf(s0, sc, lv.x)), p1 = ex2(fmaf(s1, sc, lv.y));
+              ps[e & 1] = add2(ps[e & 1], pack2(p0, p1));
             }
-            ps[e & 3] = add2(ps[e & 3], pack2(p0, p1));
           }
+          if constexpr (kMasked) ps[0] = pack2(seen[0] + seen[1], seen[2] + seen[3]);
         };
         if (partial) sweep(std::true_type{});
         else sweep(std::false_type{});
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(kBFull + st));
-        const float2 sum = unpack2(add2(add2(ps[0], ps[1]), add2(ps[2], ps[3])));
+        const float2 sum = unpack2(add2(ps[0], ps[1]));
         total += sum.x + sum.y;
       }
       // ------------------------------------------------------------ the part's sum
