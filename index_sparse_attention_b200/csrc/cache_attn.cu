@@ -24,8 +24,8 @@
 // running maximum moves only when a row's exceeds it by 8 (factors up to 2^8 in P, O and l).
 // What bounds it: HBM where the caches are long (64 sequences of 4096 keys, 8 KV heads, D=128:
 // 165 us, 6.5 TB/s, the copy bandwidth measured on this GPU); the softmax warps' chain on prefix
-// tiles of many rows (2250 cycles per 128 x 128 tile, of which the exponentials 1200 and the MMAs
-// 1050: 256 sequences over a prefix of 8192, 92 us, 375 TFLOP/s); on short calls the launches,
+// tiles of many rows (2200 cycles per 128 x 128 tile, of which the exponentials 1200 and the MMAs
+// 1050: 256 sequences over a prefix of 8192, 89 us, 385 TFLOP/s); on short calls the launches,
 // the set-up (lengths, plan, first loads: about 5 us) and the join (3 us).
 // Tried without gain: a third K stage; both softmax groups with a tile and an O of their own by
 // turns (2250 cycles a tile again: then the MMA warp's waits and issues bound); an eighth to a
@@ -354,15 +354,18 @@ __global__ void __launch_bounds__(352, 1)
         }
       }
       const float m_eff = m_run == -INFINITY ? 0.f : m_run;
-      float ps[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t ps[2] = {0ull, 0ull};  // pairs of sums
       uint32_t pk[NC / 2];
 #pragma unroll
       for (int e = 0; e < NC / 2; ++e) {
-        const float p0 = ex2(fmaf(x[2 * e], sc, -m_eff)), p1 = ex2(fmaf(x[2 * e + 1], sc, -m_eff));
-        ps[e & 3] += p0 + p1;
+        const float2 t =
+            unpack2(fma2(pack2(x[2 * e], x[2 * e + 1]), pack2(sc, sc), pack2(-m_eff, -m_eff)));
+        const float p0 = ex2(t.x), p1 = ex2(t.y);
+        ps[e & 1] = add2(ps[e & 1], pack2(p0, p1));
         pk[e] = pack_bf16x2(p0, p1);
       }
-      l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+      const float2 sum = unpack2(add2(ps[0], ps[1]));
+      l_run += sum.x + sum.y;
       if constexpr (NC >= 32) {
 #pragma unroll
         for (int j = 0; j < NC / 32; ++j) tmem_st16(scol + (c0 >> 1) + 16 * j, pk + 16 * j);
