@@ -89,11 +89,11 @@ def _check(name, t, dtype, shape=None, ndim=None, device=None, contiguous=True):
         _require(t.device == device, f"{name} is on {t.device}, expected {device}")
 
 
-def _fits(t, dtype, shape, device):
-    """Whether a tensor passes _check with these (the fast way through a call's checks: one
-    expression per tensor, and _check to say what is wrong where one fails)."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device and t.is_cuda and t.is_contiguous())
+def _fits(t, dtype, shape, index):
+    """Whether a tensor passes _check with these on CUDA device `index` (the fast way through a
+    call's checks: one expression per tensor, and _check to say what is wrong where one fails)."""
+    return (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype
+            and t.shape == shape and t.is_contiguous())
 
 
 def _check_status(dev_status, device):
@@ -375,7 +375,9 @@ def _cache_args_fit(q, k_cache, v_cache, lens, k_prefix, v_prefix, weights, weig
     if not (isinstance(q, torch.Tensor) and q.dim() == 4 and isinstance(v_cache, torch.Tensor)
             and v_cache.dim() == 4 and dev_status is None):
         return False
-    bf16, dev = torch.bfloat16, q.device
+    bf16, dev = torch.bfloat16, q.get_device()
+    if dev < 0:
+        return False
     B, T, HQ, Dqk = q.shape
     _, S, HK, Dv = v_cache.shape
     if not (_fits(q, bf16, (B, 1, HQ, Dqk), dev) and _fits(k_cache, bf16, (B, S, HK, Dqk), dev)
@@ -523,8 +525,9 @@ def cache_evict(k_cache, v_cache, weights, lens, budget, sinks=0, recent=0, k_ou
     dev = k_cache.device
     _check("v_cache", v_cache, bf16, ndim=4, device=dev)
     Dv = v_cache.shape[3]
-    if not (_fits(v_cache, bf16, (B, S, HK, Dv), dev) and _fits(weights, f32, (B, HK, S), dev)
-            and _fits(lens, i32, (B,), dev)):
+    index = dev.index
+    if not (_fits(v_cache, bf16, (B, S, HK, Dv), index) and _fits(weights, f32, (B, HK, S), index)
+            and _fits(lens, i32, (B,), index)):
         _check("v_cache", v_cache, bf16, shape=(B, S, HK, Dv), device=dev)
         _check("weights", weights, f32, shape=(B, HK, S), device=dev)
         _check("lens", lens, i32, shape=(B,), device=dev)
