@@ -287,6 +287,10 @@ __device__ __forceinline__ bool named_bar_and(int id, int nthreads, bool v) {
       : "memory");
   return r != 0;
 }
+// Asks for `bytes` at p to be brought into L2 (both multiples of 16); returns at once.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
