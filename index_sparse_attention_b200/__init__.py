@@ -445,7 +445,9 @@ def cache_attn_fwd(q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None, soft
         raise ValueError("weights needs with_weights or a weights_out")
     B, HQ, HK, Dv, S, dev = p.B, p.HQ, p.HK, p.Dv, p.S, q.device
     if o is None:
-        o = torch.empty(B, 1, HQ, Dv, dtype=torch.bfloat16, device=dev)
+        # (empty_like, where the shape is the same, takes three quarters of empty's host time)
+        o = (torch.empty_like(q) if Dv == p.Dqk
+             else torch.empty(B, 1, HQ, Dv, dtype=torch.bfloat16, device=dev))
         p.o = o.data_ptr()
     if lse is None:
         lse = torch.empty(B, HQ, 1, dtype=torch.float32, device=dev)
@@ -546,18 +548,22 @@ def cache_evict(k_cache, v_cache, weights, lens, budget, sinks=0, recent=0, k_ou
     if sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("sinks and recent must be non-negative with a sum of at most "
                          f"budget={budget}, got {sinks} and {recent}")
+    # (empty_like, where the shape is the same, takes three quarters of empty's host time)
     if k_out is None:
-        k_out = torch.empty(B, S_out, HK, Dqk, dtype=bf16, device=dev)
+        k_out = (torch.empty_like(k_cache) if S_out == S
+                 else torch.empty(B, S_out, HK, Dqk, dtype=bf16, device=dev))
     if v_out is None:
-        v_out = torch.empty(B, S_out, HK, Dv, dtype=bf16, device=dev)
+        v_out = (torch.empty_like(v_cache) if S_out == S
+                 else torch.empty(B, S_out, HK, Dv, dtype=bf16, device=dev))
     else:
         _check("v_out", v_out, bf16, shape=(B, S_out, HK, Dv), device=dev)
     if weights_out is None:
-        weights_out = torch.empty(B, HK, S_out, dtype=f32, device=dev)
+        weights_out = (torch.empty_like(weights) if S_out == S
+                       else torch.empty(B, HK, S_out, dtype=f32, device=dev))
     else:
         _check("weights_out", weights_out, f32, shape=(B, HK, S_out), device=dev)
     if lens_out is None:
-        lens_out = torch.empty(B, dtype=i32, device=dev)
+        lens_out = torch.empty_like(lens)
     else:
         _check("lens_out", lens_out, i32, shape=(B,), device=dev)
     if keep is None:
