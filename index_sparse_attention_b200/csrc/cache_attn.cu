@@ -41,12 +41,15 @@ namespace cache {
 
 template <int DQK, int DV>
 struct Cfg {
-  static constexpr int kN = DQK <= 128 ? 128 : 64;  // keys of a tile
-  // Q buffers: part p uses buffer p % 2; at head dims 256 there is one, in which the copies of up
-  // to 16 rows take rows [0, 16) or [16, 32) of each lane quarter by turns
-  static constexpr int kQBufs = DQK == 256 ? 1 : 2;
+  // keys of a tile (at head dims 192/128 128 keys take all shared memory; with 64, a second Q
+  // buffer and a third V stage: 32 sequences over 16384 keys 46.4 us against 38.8, 16 of 8192
+  // 70.7 against 65.1)
+  static constexpr int kN = DQK <= 192 ? 128 : 64;
+  // Q buffers: part p uses buffer p % 2; from head dim 192 on there is one, in which the copies of
+  // up to 16 rows take rows [0, 16) or [16, 32) of each lane quarter by turns
+  static constexpr int kQBufs = DQK >= 192 ? 1 : 2;
   static constexpr int kKStages = DQK == 64 ? 5 : 2;  // (a third one measured no faster)
-  static constexpr int kVStages = DQK == 64 ? 5 : DQK == 192 ? 3 : 2;
+  static constexpr int kVStages = DQK == 64 ? 5 : 2;
   static constexpr int kQPanel = 128 * 128;  // 64 columns x 128 rows
   static constexpr int kKPanel = kN * 128;   // 64 columns x kN rows (V too)
   static constexpr int kQBytes = 128 * DQK * 2;
@@ -58,11 +61,12 @@ struct Cfg {
   // (a barrier of the pair lies between one use's reads and the next one's writes)
   static constexpr int kXOff = kVOff + kVStages * kVBytes;
   static constexpr int kMOff = kXOff + 1024;  // a part's row maxima, [128]
-  // where the four copies of a row meet at a part's end: [2 column halves][4][32 rows][32 columns]
+  // where the four copies of a row meet at a part's end: [2 column halves][4][32 rows][kCols]
+  static constexpr int kCols = DQK == 192 ? 16 : 32;
   static constexpr int kMergeOff = kMOff + 512;
   // (what find_range needs lies there too: every warp is past it when the first part ends)
   static constexpr int kFindOff = kMergeOff;
-  static constexpr int kBarOff = kMergeOff + 32 * 1024;
+  static constexpr int kBarOff = kMergeOff + kCols * 1024;
   static constexpr int kSmem = kBarOff + 272 + 1024;
   static constexpr int kThreads = 352;
   static constexpr uint32_t kOCol = 256;  // S / P buffers at columns 0 and 128
@@ -476,22 +480,25 @@ __global__ void __launch_bounds__(352, 1)
               l += (xch[32 * q + lane] + xch[128 + 32 * q + lane]) * ex2(xm[32 * q + lane] - me);
             mls[mine] = make_float2(mm, l);
           }
-          // up to eight rows: all columns of this half at once, else 32 at a time
-          float* stage = reinterpret_cast<float*>(smem + C::kMergeOff + hc * 16384);
-          const int cp = rows <= 8 ? DV / 2 : 32;
+          // up to eight rows: all columns of this half at once, else kCols at a time
+          constexpr int kCols = C::kCols;
+          static_assert(kCols * 512 >= 4 * 8 * (DV / 2) * 4, "eight rows, half the columns");
+          float* stage = reinterpret_cast<float*>(smem + C::kMergeOff + hc * kCols * 512);
+          const int cp = rows <= 8 ? DV / 2 : kCols;
 #pragma unroll 1
           for (int c0 = hc * (DV / 2); c0 < (hc + 1) * (DV / 2); c0 += cp) {
             if (c0 != hc * (DV / 2)) named_bar_sync(6 + hc, 128);  // the last pass is read
 #pragma unroll 1
-            for (int c = 0; c < cp; c += 32) {
-              uint32_t ov[32];
-              tmem_ld32(tl + C::kOCol + c0 + c, ov);
+            for (int c = 0; c < cp; c += kCols) {
+              uint32_t ov[kCols];
+              if constexpr (kCols == 32) tmem_ld32(tl + C::kOCol + c0 + c, ov);
+              else tmem_ld16(tl + C::kOCol + c0 + c, ov);
               tmem_wait_ld();
               if (active) {
                 float4* dst = reinterpret_cast<float4*>(stage + (quarter * rows + mine) * cp + c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  dst[e ^ (mine & 7)] = make_float4(
+                for (int e = 0; e < kCols / 4; ++e)  // (turned by the row: bank conflicts)
+                  dst[e ^ (mine & (kCols / 4 - 1))] = make_float4(
                       __uint_as_float(ov[4 * e]) * f, __uint_as_float(ov[4 * e + 1]) * f,
                       __uint_as_float(ov[4 * e + 2]) * f, __uint_as_float(ov[4 * e + 3]) * f);
               }
@@ -504,7 +511,7 @@ __global__ void __launch_bounds__(352, 1)
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const float4 x = *reinterpret_cast<const float4*>(
-                    stage + (q * rows + row) * cp + 4 * (ch ^ (row & 7)));
+                    stage + (q * rows + row) * cp + 4 * (ch ^ (row & (kCols / 4 - 1))));
                 o.x += x.x;
                 o.y += x.y;
                 o.z += x.z;
@@ -757,7 +764,7 @@ static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
   a->Dv = p->Dv;
   a->S = p->S;
   a->P = p->P;
-  a->kshift = p->Dqk <= 128 ? 7 : 6;
+  a->kshift = p->Dqk <= 192 ? 7 : 6;
   a->Sp = (p->S + 127) / 128 * 128;
   a->nb = 128 / a->G;
   if (a->nb > p->B) a->nb = p->B;
@@ -769,8 +776,8 @@ static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
   a->rep_c = a->rows_c <= 32 ? 4 : 1;
   // in hundreds of cycles, measured: a tile of few rows takes what its keys take from HBM, one of
   // many rows its exponentials
-  const int many = p->Dqk == 64 ? 22 : p->Dqk == 192 ? 19 : 27;
-  const int few = p->Dqk == 64 ? 12 : p->Dqk == 192 ? 15 : 24;
+  const int many = p->Dqk == 64 ? 22 : p->Dqk == 192 ? 29 : 27;
+  const int few = p->Dqk == 64 ? 12 : p->Dqk == 192 ? 25 : 24;
   a->wt_p = a->rep_p > 1 ? few : many;
   a->wt_c = a->rep_c > 1 ? few : many;
   a->we = 30;
