@@ -573,6 +573,7 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   __shared__ float sh_o[kW > 1 ? kW : 1][DV];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = kW > 1 ? tid >> 5 : 0;
+  allow_next_kernel();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kW > 1 ? 0 : tid >> 5);
   if (row >= static_cast<int64_t>(a.B) * a.HQ) return;  // (kW == 1 only: a whole warp)
   const int b = static_cast<int>(row / a.HQ), h = static_cast<int>(row - static_cast<int64_t>(b) * a.HQ);
@@ -696,6 +697,7 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
 __global__ void __launch_bounds__(256) cache_weights_kernel(const Args a) {
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int hk = blockIdx.y, b = blockIdx.z;
+  allow_next_kernel();
   if (j >= a.S) return;  // (a block that leaves early has nothing to wait for)
   const int64_t at = (static_cast<int64_t>(b) * a.HK + hk) * a.S + j;
   const bool live = j < clamped_len(a, b);

@@ -350,6 +350,7 @@ __device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* 
 }
 __global__ void __launch_bounds__(256) evict_copy_kernel(const Args a) {
   const int b = blockIdx.y;
+  allow_next_kernel();
   wait_previous_kernel();
   const int n_out = static_cast<int>(min64(max64(static_cast<int64_t>(ld_behind(a.lens + b)), 0),
                                            min64(a.S, a.budget)));

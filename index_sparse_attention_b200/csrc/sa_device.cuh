@@ -411,7 +411,9 @@ __device__ __forceinline__ void tmem_wait_st() {
 // ---------------------------------------------------------------------------------
 // Programmatic dependent launch (launch_early in sa_kernels.h): a kernel so launched may start
 // while the one before it in the stream still runs, and reads nothing that one writes (and
-// writes nothing that one reads) before wait_previous_kernel().
+// writes nothing that one reads) before wait_previous_kernel().  That wait is for the whole of
+// the kernel before, which in turn has waited for the one before it: every kernel of a chain
+// waits, in at least one of its blocks, even if it could do without.
 // ---------------------------------------------------------------------------------
 __device__ __forceinline__ void wait_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
