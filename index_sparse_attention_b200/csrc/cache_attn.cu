@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(352, 1)
   }
   tc_fence_before();
   wait_previous_kernel();
-  allow_next_kernel();
   if (warp == 10 && lane < 2 && a.P > 0) {
     // HBM has nothing to do while the plan is made: the head of an even share of the prefix goes
     // to L2 meanwhile (16 sequences over 8192 keys 37.5 -> 36.4 us; as much before the wait, and
@@ -528,6 +527,7 @@ __global__ void __launch_bounds__(352, 1)
     }
   }
 
+  allow_next_kernel();  // (not before: the join's blocks, waiting, would take issue slots)
   tc_fence_before();
   __syncthreads();
   // Abort path: no warp issues anything past the barrier above.  Wait (with a limit) for the

@@ -91,7 +91,6 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
   const int64_t row = blockIdx.x / cl;
   const int b = static_cast<int>(row / a.HK), hk = static_cast<int>(row - static_cast<int64_t>(b) * a.HK);
   wait_previous_kernel();
-  allow_next_kernel();
   const int raw = ld_behind(a.lens + b);  // (every other load depends on it)
   const int n = static_cast<int>(min64(max64(static_cast<int64_t>(raw), 0), a.S));
   if (tid == 0 && hk == 0 && rank == 0) {
@@ -320,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
     in_before += __popc(ins);
     eq_before += __popc(eqs);
   }
+  allow_next_kernel();
   meet();  // (no CTA leaves while another may read its counts)
 }
 

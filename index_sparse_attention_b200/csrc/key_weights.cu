@@ -160,8 +160,9 @@ __device__ __forceinline__ Found find_range(const Args& a, int c, int64_t* sh) {
   const int per = (a.items + kThreads - 1) / kThreads;
   const int i0 = min(tid * per, a.items), i1 = min(i0 + per, a.items);
   auto entries = [&](int i) {
-    return __ldg(a.t.tcnt + 2 * static_cast<int64_t>(i)) +
-           __ldg(a.t.tcnt + 2 * static_cast<int64_t>(i) + 1);
+    // (every other load depends on these)
+    return ld_behind(a.t.tcnt + 2 * static_cast<int64_t>(i)) +
+           ld_behind(a.t.tcnt + 2 * static_cast<int64_t>(i) + 1);
   };
   int64_t len = 0, num = 0;  // of this thread's items: length, list entries
 #pragma unroll 4
@@ -265,6 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  wait_previous_kernel();
+  // (the join is not let in early: its blocks, waiting, slow the exponentials: 104.8 us for the
+  // causal prompt against 100.6)
   const Found f = find_range(ka, cta, reinterpret_cast<int64_t*>(smem + C::kFindOff));
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
@@ -574,6 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(128) key_weights_join_kernel(const Args ka) {
   const AttnArgs& a = ka.t;
   const int r = threadIdx.x, c = blockIdx.x;
+  allow_next_kernel();
+  wait_previous_kernel();
   auto store = [&](int item, float sum) {
     const int bg = item / a.Tn;
     const int64_t j = static_cast<int64_t>(item - bg * a.Tn) * 128 + r;
@@ -605,8 +611,8 @@ static int launch(const Args& a, const CUtensorMap& mq, const CUtensorMap& mk, c
                       "key weights smem attribute");
   });
   if (rc) return rc;
-  key_weights_kernel<DQK><<<a.C, kThreads, C::kSmem, st>>>(mq, mk, a);
-  return check_launch("key weights kernel launch");
+  return launch_early(key_weights_kernel<DQK>, dim3(a.C), dim3(kThreads), C::kSmem, st,
+                      "key weights kernel launch", 1, mq, mk, a);
 }
 
 }  // namespace kweights
@@ -660,6 +666,7 @@ extern "C" int sparse_attn_key_weights(const sparse_attn_params* p, const float*
   else if (p->Dqk == 192) rc = kweights::launch<192>(a, mq, mk, st);
   else rc = kweights::launch<256>(a, mq, mk, st);
   if (rc) return rc;
-  kweights::key_weights_join_kernel<<<static_cast<unsigned>(a.C + (a.items + 31) / 32), 128, 0, st>>>(a);
-  return check_launch("key weights join kernel launch");
+  return launch_early(kweights::key_weights_join_kernel,
+                      dim3(static_cast<unsigned>(a.C + (a.items + 31) / 32)), dim3(128), 0, st,
+                      "key weights join kernel launch", 1, a);
 }
