@@ -19,7 +19,9 @@
 //              for 32 rows of 65536 (with the slice in shared memory and 64-bit positions 39).
 //   copy       16-byte pieces, four rows per thread in flight, writes contiguous over all heads
 //              of a row.  Bound by HBM (each kept row is read and written once): 16 sequences of
-//              8 heads cut from 8191 to 2048 keys, D=128, 56 us in all, 4.7 TB/s of its bytes.
+//              8 heads cut from 8191 to 2048 keys, D=128, 55 us in all, 4.8 TB/s of its bytes.
+//              (Asking L2 for the rows that are sure to stay while the selection still runs
+//              made it slower, 57 us: its warps have no time for that.)
 #include "sa_device.cuh"
 #include "sa_kernels.h"
 

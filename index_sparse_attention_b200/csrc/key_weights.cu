@@ -24,8 +24,8 @@
 //   warp 18    feeds the units' lse values and list entries through shared memory.
 // What bounds it: the special-function unit.  A unit's 16384 exponentials take an SM 1024 cycles
 // (its MMAs 512 at head dim 128); measured 1300 to 1400 cycles a unit on long prompts (101 us for
-// the causal prompt B=2 H=16 S=4096 D=128, 679 TFLOP/s of allowed pairs; 104 us for the
-// block-sparse one with 32 / 8 heads, S=8192; 113 us for the index prompt with 32 / 4 heads,
+// the causal prompt B=2 H=16 S=4096 D=128, 684 TFLOP/s of allowed pairs; 103 us for the
+// block-sparse one with 32 / 8 heads, S=8192; 111 us for the index prompt with 32 / 4 heads,
 // S=4001, head dims 192/128).  Tried and slower: a unit per warpgroup (a group stands idle while
 // its buffer is refilled), eight warps with half a unit each and the next half's TMEM loads in
 // flight (the remaining latency of a unit is shared by fewer warps), an eighth to a half of the
