@@ -1,8 +1,8 @@
 // cache_evict.cu -- eviction from a cache by accumulated attention weight (cache_evict).
 //
 // Per (sequence, KV head) of n > budget keys: the first `sinks`, the last `recent` and the
-// budget - sinks - recent heaviest keys between them stay, in their order.  Two launches:
-// selection (which positions stay) and the copy of the kept rows.
+// budget - sinks - recent heaviest keys between them stay, in their order.  First the selection
+// (which positions stay), then the copy of the kept rows.
 //   selection  a cluster of 1 to 8 CTAs per (sequence, KV head), a slice of the row each, held
 //              in registers as order-preserving keys (4, 8 or 16 per thread; longer slices are
 //              read again in every sweep).  Radix select of the smallest kept weight in up to
@@ -17,11 +17,12 @@
 //              the threshold, and of those equal to it the first ones that are still needed.
 //              Bound by the sweeps' instructions and the cluster's meetings, not by bytes: 25 us
 //              for 32 rows of 65536 (with the slice in shared memory and 64-bit positions 39).
-//   copy       16-byte pieces, four rows per thread in flight, writes contiguous over all heads
-//              of a row.  Bound by HBM (each kept row is read and written once): 16 sequences of
-//              8 heads cut from 8191 to 2048 keys, D=128, 55 us in all, 4.8 TB/s of its bytes.
-//              (Asking L2 for the rows that are sure to stay while the selection still runs
-//              made it slower, 57 us: its warps have no time for that.)
+//   copy       16-byte pieces, four rows per thread in flight; by the selection's own CTAs where
+//              they fill the SMs, else by a kernel of its own (writes contiguous over all heads
+//              of a row).  Bound by HBM (each kept row is read and written once): 16 sequences of
+//              8 heads cut from 8191 to 2048 keys, D=128, 52 us in all, 5.1 TB/s of its bytes.
+//              (Asking L2 for the rows that are sure to stay while the selection still runs made
+//              it slower: its warps have no time for that.)
 #include "sa_device.cuh"
 #include "sa_kernels.h"
 
@@ -36,6 +37,7 @@ constexpr int kPerThread = kBins / kThreads;
 constexpr int kSlice = 8192;        // keys a CTA takes before the row is spread over more of them
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCtas = 128;       // CTAs that run at once (clusters do not fill every SM)
+constexpr int kSms = 148;
 
 struct Args {
   const uint4 *k, *v;
@@ -49,6 +51,7 @@ struct Args {
   int budget, sinks, recent;
   int cluster;
   int rows;  // of a CTA of the copy
+  bool fused;  // the selection's CTAs copy the rows themselves
   int32_t* status;
 };
 
@@ -82,6 +85,34 @@ __device__ __forceinline__ int warp_scan(int x) {
 }
 
 // KPT: keys per thread held in registers; 0: read from memory in every sweep.
+// The kept rows of one (sequence, KV head), this CTA's share of them: 16-byte pieces, four rows
+// per thread in flight.  keep null: row i is row i.
+template <int kN>
+__device__ __forceinline__ void copy_head(const uint4* __restrict__ src, uint4* __restrict__ dst,
+                                          const int32_t* keep, int64_t pitch, int per_head, int n,
+                                          int rank, int cl) {
+  const int at_once = kThreads / per_head, r = threadIdx.x / per_head,
+            p = threadIdx.x - r * per_head;
+  if (r >= at_once) return;
+  const int step = at_once * cl;
+  for (int i0 = rank * at_once + r; i0 < n; i0 += kN * step) {
+    int64_t from[kN];
+    uint4 x[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const int i = i0 + e * step;
+      from[e] = i;
+      if (i < n && keep) from[e] = keep[i];
+    }
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (i0 + e * step < n) x[e] = __ldg(src + from[e] * pitch + p);
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (i0 + e * step < n) dst[(i0 + e * step) * pitch + p] = x[e];
+  }
+}
+
 template <int KPT>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a) {
   __shared__ __align__(16) int own[kBins], all[kBins];  // own counts of a digit, the cluster's
@@ -108,12 +139,20 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
     for (int64_t i = n_out + first; i < a.So; i += step) wo[i] = 0.f;
     for (int i = n_out + first; i < a.budget; i += step) keep[i] = -1;
   };
+  auto copy_all = [&](const int32_t* from) {
+    const int64_t pk = static_cast<int64_t>(a.HK) * a.kp, pv = static_cast<int64_t>(a.HK) * a.vp;
+    copy_head<4>(a.k + b * a.S * pk + hk * a.kp, a.ko + b * a.So * pk + hk * a.kp, from, pk, a.kp,
+                 n_out, rank, cl);
+    copy_head<4>(a.v + b * a.S * pv + hk * a.vp, a.vo + b * a.So * pv + hk * a.vp, from, pv, a.vp,
+                 n_out, rank, cl);
+  };
   if (n <= a.budget) {  // (the same on every CTA of the cluster)
     for (int i = first; i < n_out; i += step) {
       keep[i] = i;
       wo[i] = __ldg(w + i);
     }
     fill_tails();
+    if (a.fused) copy_all(nullptr);
     return;
   }
   const int lo = a.sinks, hi = n - a.recent;         // the candidates
@@ -321,8 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
     in_before += __popc(ins);
     eq_before += __popc(eqs);
   }
-  allow_next_kernel();
-  meet();  // (no CTA leaves while another may read its counts)
+  if (!a.fused) allow_next_kernel();
+  meet();  // (no CTA leaves while another may read its counts; keep is written)
+  if (a.fused) copy_all(keep);
 }
 
 // One CTA per a.rows output rows of a sequence; a thread keeps its 16-byte column of a row and
@@ -429,7 +469,7 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
   a.status = p->dev_status;
   // rows of a copy CTA: 16, or 4 (one round of loads) where that leaves SMs without work
   const int64_t most = min64(p->budget, p->S);
-  a.rows = (most + 15) / 16 * p->B >= 4 * 148 ? 16 : 4;
+  a.rows = (most + 15) / 16 * p->B >= 4 * evict::kSms ? 16 : 4;
   // A row is spread over more CTAs while its slices are long, as long as all clusters run at
   // once (32 rows of 65536 over 256 CTAs: 56 us; one row's cluster alone takes 20), or until a
   // slice fits in registers.
@@ -439,6 +479,13 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
           (static_cast<int64_t>(a.cluster) * evict::kSlice < p->S &&
            BH * a.cluster * 2 <= evict::kMaxCtas)))
     a.cluster *= 2;
+  // Selection CTAs that fill the SMs copy their own rows (no second launch, and rows that are
+  // selected early are copied while others are not): 64 sequences of 8 heads, 8191 to 2048 keys,
+  // D=128, 191 us against 208, 16 of them 57 against 60.  Few CTAs, or a last wave of them that
+  // leaves SMs idle, would copy with part of the GPU: 2 sequences of 131072 84 us against 77, 20
+  // of 8191 (160 CTAs) 88 against 76.
+  const int64_t ctas = BH * a.cluster, waves = (ctas + evict::kSms - 1) / evict::kSms;
+  a.fused = ctas * 5 >= waves * evict::kSms * 4;
   if (BH * a.cluster > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
   // keys per thread: a warp's stretch of the longest slice, in whole 32s
   const int64_t slice = ((p->S + a.cluster - 1) / a.cluster + 31) / 32 * 32;
@@ -450,6 +497,7 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
   rc = launch_early(select, dim3(static_cast<unsigned>(BH * a.cluster)), dim3(evict::kThreads), 0, st,
                     "eviction select kernel launch", a.cluster, a);
   if (rc) return rc;
+  if (a.fused) return SA_OK;
   return launch_early(evict::evict_copy_kernel,
                       dim3(static_cast<unsigned>((most + a.rows - 1) / a.rows),
                            static_cast<unsigned>(p->B)),

@@ -95,6 +95,13 @@ CASES = {
     "nan_inf": dict(lens=[3000, 2999], HK=2, D=D64, S=3000, budget=200, sinks=2, recent=5, weights=special),
     "low_bits": dict(lens=[3000, 2999], HK=2, D=D64, S=3000, budget=1200, weights=close),
     "many_rows": dict(lens=[20 + i for i in range(50)], HK=8, D=D64, S=70, budget=33, sinks=1, recent=8),
+    # as many rows as SMs, so that the selection copies its own: short and long ones, every head dim
+    "own_copy_d64": dict(lens=[300, 301, 0, 1, 299, 700, 512, 90] * 3, HK=5, D=D64, S=700, budget=300, sinks=4, recent=20),
+    "own_copy_d128": dict(lens=[40 + 7 * i for i in range(18)], HK=8, D=D128, S=160, budget=101, recent=9),
+    "own_copy_d192": dict(lens=[33, 200, 201, 57] * 8, HK=4, D=D192, S=201, budget=57, sinks=3),
+    "own_copy_d256": dict(lens=[20 + i for i in range(140)], HK=1, D=D256, S=160, budget=37, sinks=1, recent=1),
+    "own_copy_cluster": dict(lens=[9001 - 500 * i for i in range(16)], HK=4, D=D64, S=9001, budget=1203, sinks=4, recent=64),
+    "own_copy_of_ties": dict(lens=[400 - i for i in range(72)], HK=2, D=D64, S=400, budget=150, sinks=2, recent=3, weights=ties),
 }
 
 
