@@ -815,6 +815,8 @@ static int check(const cache_attn_params* p) {
   if (static_cast<int64_t>(p->B) * p->HQ > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
   if (p->B > 65535 || p->HQ > 65535 || p->S > 0x7FFFFF00 || p->P > 0x7FFFFF00)
     return SA_ERR_UNSUPPORTED;
+  // (beyond any memory; keeps the workspace's size in range)
+  if (p->S > (int64_t(1) << 40) / (static_cast<int64_t>(p->B) * p->HQ)) return SA_ERR_UNSUPPORTED;
   return SA_OK;
 }
 
@@ -841,6 +843,9 @@ extern "C" int cache_attn_fwd(const cache_attn_params* p, void* workspace, size_
   const void* ptrs[] = {p->q, p->k_cache, p->v_cache, p->k_prefix, p->v_prefix, p->o};
   for (const void* x : ptrs)
     if ((reinterpret_cast<uintptr_t>(x) & 15u) != 0) return SA_ERR_ALIGN;
+  const void* words[] = {p->lens, p->lse, p->weights, p->weights_out, p->dev_status};
+  for (const void* x : words)
+    if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return SA_ERR_ALIGN;
   cache::Args a{};
   const size_t need = cache::lay_out(p, &a, static_cast<char*>(workspace));
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)

@@ -444,6 +444,9 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
   const void* ptrs[] = {p->k_cache, p->v_cache, p->k_out, p->v_out};
   for (const void* x : ptrs)
     if ((reinterpret_cast<uintptr_t>(x) & 15u) != 0) return SA_ERR_ALIGN;
+  const void* words[] = {p->weights, p->lens, p->weights_out, p->lens_out, p->keep, p->dev_status};
+  for (const void* x : words)
+    if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return SA_ERR_ALIGN;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int rc = check_stream_device(st);
   if (rc) return rc;

@@ -638,6 +638,9 @@ extern "C" int sparse_attn_key_weights(const sparse_attn_params* p, const float*
   int rc = fill_args(&fake, &a.t, false);
   if (rc) return rc;
   if (!weights_out) return SA_ERR_INVALID;
+  const void* words[] = {p->lse, weights, weights_out, p->dev_status};
+  for (const void* x : words)
+    if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return SA_ERR_ALIGN;
   const int64_t items = static_cast<int64_t>(p->B) * p->HK * a.t.Tn;
   if (items * a.t.Tm > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
   const size_t need = sparse_attn_key_weights_workspace_size(p);

@@ -42,7 +42,8 @@ def call_attn(lib, p, ws=0x100000, n=1 << 40):
     (dict(HQ=258, HK=2), UNSUP), (dict(S=1 << 40), UNSUP), (dict(P=1 << 40), UNSUP),
     (dict(B=65536), UNSUP), (dict(B=65535, HQ=65535, HK=65535), UNSUP),
     (dict(q=0x1008), _lib.SA_ERR_ALIGN), (dict(k_prefix=0x5008), _lib.SA_ERR_ALIGN),
-    (dict(o=0x7004), _lib.SA_ERR_ALIGN),
+    (dict(o=0x7004), _lib.SA_ERR_ALIGN), (dict(lens=0x4002), _lib.SA_ERR_ALIGN),
+    (dict(lse=0x8001), _lib.SA_ERR_ALIGN), (dict(weights_out=0x9002), _lib.SA_ERR_ALIGN),
 ], ids=str)
 def test_attention_refusals(lib, kw, code):
     assert call_attn(lib, attn(**kw)) == code
@@ -59,6 +60,10 @@ def test_attention_workspace_is_checked(lib):
     more = lib.cache_attn_workspace_size(ctypes.byref(attn(weights_out=0x9000)))
     assert more == need + 2 * 8 * 128 * 4  # the scores [B][HQ][ceil(S / 128) * 128]
     assert lib.cache_attn_workspace_size(ctypes.byref(attn(B=0))) == 0
+    # sizes whose products pass 64 bits are refused before any of them is taken
+    huge = attn(B=65535, HQ=65535, HK=65535, S=0x7FFFFF00, weights_out=0x9000)
+    assert lib.cache_attn_workspace_size(ctypes.byref(huge)) == 0
+    assert lib.cache_attn_fwd(ctypes.byref(huge), 0x10000, 1 << 40, None) == UNSUP
 
 
 def test_key_weights_refusals(lib):
@@ -78,6 +83,7 @@ def test_key_weights_refusals(lib):
         assert call(**kw) == BAD, kw
     assert call(Dqk=96) == UNSUP
     assert call(q=0x1008) == _lib.SA_ERR_ALIGN
+    assert call(lse=0x1002) == _lib.SA_ERR_ALIGN and call(out=0x9001) == _lib.SA_ERR_ALIGN
     assert lib.sparse_attn_key_weights(None, None, 0x9000, None, 0, None) == BAD
     p = _lib.ParamsStruct(0x1000, 0x1000, None, None, 0x1000, None, None, None, None, 1, 4, 2, 128,
                           128, 256, 256, 0.125, ctypes.pointer(s), None)
@@ -100,6 +106,7 @@ def test_key_weights_refusals(lib):
     (dict(lens_out=0x400000), BAD), (dict(k_out=0x100000 + 102384), BAD),
     (dict(v_out=0x500000 - 102384), BAD), (dict(keep=0x700010), BAD), (dict(Dqk=80), UNSUP), (dict(B=65536), UNSUP),
     (dict(S=1 << 40), UNSUP), (dict(k_cache=0x100008), _lib.SA_ERR_ALIGN),
+    (dict(weights=0x300002), _lib.SA_ERR_ALIGN), (dict(keep=0x900001), _lib.SA_ERR_ALIGN),
 ], ids=str)
 def test_eviction_refusals(lib, kw, code):
     p = _lib.CacheEvictStruct(0x100000, 0x200000, 0x300000, 0x400000, 0x500000, 0x600000, 0x700000,
