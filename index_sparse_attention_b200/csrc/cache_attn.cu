@@ -57,17 +57,22 @@ struct Cfg {
   static constexpr int kVBytes = kN * DV * 2;
   static constexpr int kKOff = kQBufs * kQBytes;
   static constexpr int kVOff = kKOff + kKStages * kKBytes;
-  // what the two warps of a quarter exchange, [2][128]: a tile's row maxima, a part's row sums
-  // (a barrier of the pair lies between one use's reads and the next one's writes)
+  // What the two warps of a quarter exchange, two buffers of [2 warps][128 rows]: tile `it` puts
+  // its row maxima into buffer it % 2.  The pair's barrier lies between a tile's writes and its
+  // reads, and that of the next tile between those reads and the writes of the tile after it
+  // (with one buffer nothing did: S of the next tile may be there before P of this one, and a
+  // warp would write its next maximum while the other still had to read this one).  A part that
+  // ends with tile `it` puts its row sums into the other buffer, whose last readers are past the
+  // barrier of tile `it`, and reads them before a barrier that tile it + 1 lies behind.
   static constexpr int kXOff = kVOff + kVStages * kVBytes;
-  static constexpr int kMOff = kXOff + 1024;  // a part's row maxima, [128]
+  static constexpr int kMOff = kXOff + 2048;  // a part's row maxima, [128]
   // where the four copies of a row meet at a part's end: [2 column halves][4][32 rows][kCols]
   static constexpr int kCols = DQK == 192 ? 16 : 32;
   static constexpr int kMergeOff = kMOff + 512;
   // (what find_range needs lies there too: every warp is past it when the first part ends)
   static constexpr int kFindOff = kMergeOff;
   static constexpr int kBarOff = kMergeOff + kCols * 1024;
-  static constexpr int kSmem = kBarOff + 272 + 1024;
+  static constexpr int kSmem = kBarOff + 272;  // (the swizzled tiles' base is declared 1024-aligned)
   static constexpr int kThreads = 352;
   static constexpr uint32_t kOCol = 256;  // S / P buffers at columns 0 and 128
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -87,9 +92,7 @@ __global__ void __launch_bounds__(352, 1)
     cache_part_kernel(const __grid_constant__ Maps maps, const Args a) {
   using C = Cfg<DQK, DV>;
   constexpr int kN = C::kN;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * kNumBars);
   volatile WaitCtl* ctl =
@@ -334,11 +337,12 @@ __global__ void __launch_bounds__(352, 1)
         for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], x[NC - 4 + e]);
       }
       float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * sc;
-      xch[hc * 128 + r] = mx;
+      float* xm = xch + (it & 1) * 256;
+      xm[hc * 128 + r] = mx;
       // both warps have read their S columns past this barrier: P may be written over them
       // (one whose wait gave up has read what was there, and both leave)
       if (!both(there)) return false;
-      mx = fmaxf(xch[r], xch[128 + r]);
+      mx = fmaxf(xm[r], xm[128 + r]);
       const bool need = active && mx > m_run + 8.0f;
       const float alpha = need ? ex2(m_run - mx) : 1.f;
       if (__any_sync(0xFFFFFFFFu, need)) {
@@ -441,16 +445,17 @@ __global__ void __launch_bounds__(352, 1)
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBOF), part & 1, ctl, a.status,
                                                  a.wait_limit_ns));
         ++part;
+        float* xs = xch + ((it + 1) & 1) * 256;
+        if (hc == 1) xs[128 + r] = l_run;
         ok = named_bar_and(8, 256, ok);
         if (!ok) continue;
         tc_fence_after();
         const int64_t slot = at.seg + cta;
         float2* mls = (at.prefix ? a.ml_p : a.ml_c) + slot * rows;
         float* po = (at.prefix ? a.po_p : a.po_c) + slot * rows * DV;
-        xch[hc * 128 + r] = l_run;
         if (!rep) {
-          named_bar_sync(pair_bar, 64);
-          if (active && hc == 0) mls[r] = make_float2(m_run, xch[r] + xch[128 + r]);
+          if (active && hc == 0) mls[r] = make_float2(m_run, l_run + xs[128 + r]);
+          named_bar_sync(pair_bar, 64);  // (the next tile's maxima go where the sum was)
 #pragma unroll 1
           for (int c = hc * (DV / 2); c < (hc + 1) * (DV / 2); c += 32) {
             uint32_t ov[32];
@@ -465,7 +470,12 @@ __global__ void __launch_bounds__(352, 1)
         } else {
           // the four copies of a row (each over its own keys) become one result
           float* xm = reinterpret_cast<float*>(smem + C::kMOff);
-          if (hc == 0) xm[r] = m_run;
+          if (hc == 0) {
+            xm[r] = m_run;
+            xs[r] = l_run + xs[128 + r];
+          }
+          // (behind it nothing reads the second half of xs; the first half is read by a warp that
+          // meets the writers of the next tile's maxima, the hc == 0 warps, at the merge's barriers)
           named_bar_sync(5, 256);
           float mm = -INFINITY;
 #pragma unroll
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(352, 1)
             float l = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              l += (xch[32 * q + lane] + xch[128 + 32 * q + lane]) * ex2(xm[32 * q + lane] - me);
+              l += xs[32 * q + lane] * ex2(xm[32 * q + lane] - me);
             mls[mine] = make_float2(mm, l);
           }
           // up to eight rows: all columns of this half at once, else kCols at a time
