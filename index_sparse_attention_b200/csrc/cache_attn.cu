@@ -766,8 +766,11 @@ static int launch(const Args& a, cudaStream_t st) {
 
 static size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// The plan's sizes and the workspace's layout; returns its bytes.
+// The plan's sizes and the workspace's layout; returns its bytes.  Partial outputs are stored in
+// 32-byte pieces (st_global_v8): the layout begins at the first 32-byte boundary of a workspace
+// that need only be 16-byte aligned.
 static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
+  if (ws) ws += reinterpret_cast<uintptr_t>(ws) & 16u;
   a->B = p->B;
   a->HQ = p->HQ;
   a->HK = p->HK;
@@ -812,7 +815,7 @@ static size_t lay_out(const cache_attn_params* p, Args* a, char* ws) {
   if (p->weights_out)
     a->scores = reinterpret_cast<float*>(
         take(static_cast<size_t>(p->B) * p->HQ * static_cast<size_t>(a->Sp) * sizeof(float)));
-  return off;
+  return off + 16;
 }
 
 static int check(const cache_attn_params* p) {

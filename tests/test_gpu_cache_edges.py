@@ -1,5 +1,5 @@
 """cache_attn_fwd where its warps, its workspace and its arithmetic have their edges: row maxima
-that move by turns in either half of a tile."""
+that move by turns in either half of a tile, workspaces at every alignment that is allowed."""
 import numpy as np
 import pytest
 
@@ -68,3 +68,22 @@ def test_maxima_that_move_from_half_to_half(name):
     for _ in range(20):
         again = sa.cache_attn_fwd(**c.g, weights=w, with_weights=True)
         assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("shift", [0, 16, 48, 240])
+@pytest.mark.parametrize("D", [D64, D128, D192, D256], ids=str)
+def test_a_workspace_of_exact_size_at_any_16_byte_boundary(D, shift):
+    """A slice of a caller's pool: every part's output lies inside it, with row copies (the caches
+    here) and without (the prefix), and few bytes in front of it and behind it stay as they were."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    c = Case([300, 40, 7, 129] * 10, HQ=8, HK=2, D=D, P=700, seed=520)
+    w = torch.from_numpy(c.w).cuda()
+    need = sa.cache_attn_workspace_size(c.g["q"], c.g["k_cache"], c.g["v_cache"], c.g["lens"],
+                                        c.g["k_prefix"], c.g["v_prefix"], with_weights=True)
+    pool = torch.full((need + 1024,), 0xA5, dtype=torch.uint8, device="cuda")
+    assert pool.data_ptr() % 256 == 0
+    at = 256 + shift
+    got = sa.cache_attn_fwd(**c.g, weights=w, with_weights=True, workspace=pool[at:at + need])
+    _compare(got, *c.reference())
+    assert (pool[:at] == 0xA5).all() and (pool[at + need:] == 0xA5).all()
