@@ -84,11 +84,16 @@ __device__ __forceinline__ int warp_scan(int x) {
   return x;
 }
 
-// KPT: keys per thread held in registers; 0: read from memory in every sweep.
+// The weights, and the rows copied, may come from a kernel that let this one start before it had
+// written them (the key weights' join, a decoding step's weights, an eviction's copy): they are
+// read by coherent loads, behind wait_previous_kernel().  The read-only path (__ldg) is for data
+// that nothing writes while a kernel runs, from its start on.  From L2, since the copies read a
+// row once.
+
 // The kept rows of one (sequence, KV head), this CTA's share of them: 16-byte pieces, four rows
 // per thread in flight.  keep null: row i is row i.
 template <int kN>
-__device__ __forceinline__ void copy_head(const uint4* __restrict__ src, uint4* __restrict__ dst,
+__device__ __forceinline__ void copy_head(const uint4* src, uint4* dst,
                                           const int32_t* keep, int64_t pitch, int per_head, int n,
                                           int rank, int cl) {
   const int at_once = kThreads / per_head, r = threadIdx.x / per_head,
@@ -106,13 +111,14 @@ __device__ __forceinline__ void copy_head(const uint4* __restrict__ src, uint4* 
     }
 #pragma unroll
     for (int e = 0; e < kN; ++e)
-      if (i0 + e * step < n) x[e] = __ldg(src + from[e] * pitch + p);
+      if (i0 + e * step < n) x[e] = __ldcg(src + from[e] * pitch + p);
 #pragma unroll
     for (int e = 0; e < kN; ++e)
       if (i0 + e * step < n) dst[(i0 + e * step) * pitch + p] = x[e];
   }
 }
 
+// KPT: keys per thread held in registers; 0: read from memory in every sweep.
 template <int KPT>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a) {
   __shared__ __align__(16) int own[kBins], all[kBins];  // own counts of a digit, the cluster's
@@ -147,9 +153,17 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
                  n_out, rank, cl);
   };
   if (n <= a.budget) {  // (the same on every CTA of the cluster)
-    for (int i = first; i < n_out; i += step) {
-      keep[i] = i;
-      wo[i] = __ldg(w + i);
+    for (int i0 = first; i0 < n_out; i0 += 4 * step) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + e * step < n_out) x[e] = __ldcg(w + i0 + e * step);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + e * step < n_out) {
+          keep[i0 + e * step] = i0 + e * step;
+          wo[i0 + e * step] = x[e];
+        }
     }
     fill_tails();
     if (a.fused) copy_all(nullptr);
@@ -171,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
   if constexpr (KPT > 0) {
     float x[kHeld];
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) x[j] = w0 + 32 * j + lane < w1 ? __ldg(w + w0 + 32 * j + lane) : 0.f;
+    for (int j = 0; j < KPT; ++j) x[j] = w0 + 32 * j + lane < w1 ? __ldcg(w + w0 + 32 * j + lane) : 0.f;
     fill_tails();  // (while the loads are on their way)
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
@@ -185,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
   // the key of this lane in sweep j (position w0 + 32 j + lane, below w1)
   auto key_of = [&](int j) -> uint32_t {
     if constexpr (KPT > 0) return held[j];
-    else return weight_key(__ldg(w + w0 + 32 * j + lane));
+    else return weight_key(w[w0 + 32 * j + lane]);
   };
   auto meet = [&] {
     if (cl > 1) cluster_meet();
@@ -338,6 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
     eq_before += __reduce_add_sync(0xFFFFFFFFu, e);
   }
   const uint32_t below = (1u << lane) - 1u;
+  // the weights themselves (their own bits: -0 and every NaN share a key), all loads in flight
+  // before the first store
+  float value[kHeld];
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j)
+      if (((sure | equal) >> j) & 1u) value[j] = __ldcg(w + w0 + 32 * j + lane);
+  }
 #pragma unroll(kUnroll)
   for (int j = 0; j < sweeps; ++j) {
     const int i = w0 + 32 * j + lane;
@@ -355,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
     if (in || (eq && eq_at < need)) {
       const int at = in_before + __popc(ins & below) + min(eq_at, need);
       keep[at] = i;
-      wo[at] = __ldg(w + i);  // (its own bits: -0 and every NaN share a key)
+      if constexpr (KPT > 0) wo[at] = value[j];
+      else wo[at] = w[i];
     }
     in_before += __popc(ins);
     eq_before += __popc(eqs);
@@ -369,9 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
 // takes every 256-th, four rows at once (with eight pieces of K and V mixed per thread, and a
 // quotient for each, the large copies took half as long again).
 template <int kN>
-__device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* __restrict__ dst,
-                                          const int32_t* keep, int budget, int HK,
-                                          int per_head, int i0, int rows) {
+__device__ __forceinline__ void copy_rows(const uint4* src, uint4* dst, const int32_t* keep,
+                                          int budget, int HK, int per_head, int i0, int rows) {
   const int per_row = HK * per_head;
   for (int p = threadIdx.x; p < per_row; p += 256) {
     const int32_t* kp = keep + static_cast<int64_t>(p / per_head) * budget + i0;
@@ -383,7 +405,7 @@ __device__ __forceinline__ void copy_rows(const uint4* __restrict__ src, uint4* 
         if (r + e < rows) from[e] = kp[r + e];
 #pragma unroll
       for (int e = 0; e < kN; ++e)
-        if (r + e < rows) x[e] = __ldg(src + from[e] * per_row + p);
+        if (r + e < rows) x[e] = __ldcg(src + from[e] * per_row + p);
 #pragma unroll
       for (int e = 0; e < kN; ++e)
         if (r + e < rows) dst[static_cast<int64_t>(i0 + r + e) * per_row + p] = x[e];

@@ -1,0 +1,87 @@
+"""The cache calls one behind another without a host in between, as a server makes them: each
+starts while the one before it ends, and reads what that one wrote.  The results are those of the
+same calls with the GPU waited for after each."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+D64, D128, D192, D256 = (64, 64), (128, 128), (192, 128), (256, 256)
+
+
+def _caches(B, S, HK, D, seed):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    k = torch.randn((B, S, HK, D[0]), generator=g, device="cuda").bfloat16()
+    v = torch.randn((B, S, HK, D[1]), generator=g, device="cuda").bfloat16()
+    w = torch.rand((B, HK, S), generator=g, device="cuda")
+    lens = torch.randint(S // 2, S + 1, (B,), generator=g, device="cuda").int()
+    return g, k, v, w, lens
+
+
+# sizes that are no multiple of a sector or line, in every way that a row is selected and copied
+CHAINS = {
+    "one_cache": dict(B=1, S=333, HK=3, D=D64, budget=111, again=57),
+    "batch": dict(B=5, S=1021, HK=3, D=D128, budget=401, again=77),
+    "own_copies": dict(B=37, S=517, HK=4, D=D128, budget=201, again=99),
+    "spread_rows": dict(B=2, S=33001, HK=2, D=D64, budget=9001, again=4003),
+    "longer_than_registers": dict(B=1, S=150001, HK=1, D=D64, budget=20011, again=3001),
+    "d192": dict(B=3, S=2049, HK=2, D=D192, budget=1023, again=511),
+    "d256": dict(B=3, S=1537, HK=2, D=D256, budget=1537, again=1),
+}
+
+
+@pytest.mark.parametrize("name", CHAINS)
+def test_decode_then_evict_then_evict_again(name):
+    import torch
+    import index_sparse_attention_b200 as sa
+    c = CHAINS[name]
+    g, k, v, w0, lens = _caches(c["B"], c["S"], c["HK"], c["D"], seed=9)
+    qs = [torch.randn((c["B"], 1, 2 * c["HK"], c["D"][0]), generator=g, device="cuda").bfloat16()
+          for _ in range(12)]
+
+    def chain(q, wait):
+        w = w0.clone()
+        out = list(sa.cache_attn_fwd(q, k, v, lens, weights=w, weights_out=w))
+        wait()
+        a = sa.cache_evict(k, v, w, lens, c["budget"], sinks=1, recent=0,
+                           k_out=torch.zeros_like(k), v_out=torch.zeros_like(v))
+        wait()
+        b = sa.cache_evict(a[0], a[1], a[2], a[3], c["again"], recent=1,
+                           k_out=torch.zeros_like(k), v_out=torch.zeros_like(v))
+        wait()
+        return [*out, *a, *b]
+
+    for q in qs:
+        torch.cuda.synchronize()
+        got = chain(q, lambda: None)
+        want = chain(q, torch.cuda.synchronize)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("Sq", [129, 1000])
+def test_key_weights_then_evict(Sq):
+    """Weights of a prompt that the eviction behind them reads."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    B, S, HK, HQ = 2, 1027, 2, 8
+    g, k, v, _, _ = _caches(B, S, HK, D128, seed=19)
+    lens = torch.full((B,), S, dtype=torch.int32, device="cuda")
+    lists = sa.block_mask_to_block_sparse(None, B, HK, Sq, S)
+    qs = [torch.randn((B, Sq, HQ, 128), generator=g, device="cuda").bfloat16() for _ in range(12)]
+
+    def chain(q, wait):
+        o, lse = sa.sparse_attn_fwd(q, k, v, lists)
+        wait()
+        w = sa.sparse_attn_key_weights(q, k, lse, lists)
+        wait()
+        a = sa.cache_evict(k, v, w, lens, 301, sinks=1, recent=3, k_out=torch.zeros_like(k),
+                           v_out=torch.zeros_like(v))
+        wait()
+        return [o, lse, w, *a]
+
+    for q in qs:
+        torch.cuda.synchronize()
+        got = chain(q, lambda: None)
+        want = chain(q, torch.cuda.synchronize)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
