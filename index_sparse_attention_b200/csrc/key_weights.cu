@@ -31,7 +31,9 @@
 // flight (the remaining latency of a unit is shared by fewer warps), an eighth to a half of the
 // exponentials by a polynomial of packed fused multiply-adds (equal to slower: the warps are
 // short of issue slots and latency, not of that unit alone).
-// Every mbarrier wait is bounded (sa_device.cuh).
+// Every mbarrier wait is bounded (sa_device.cuh).  The kernels start while the one ahead of them
+// ends: what that one may still be writing (an lse that cache_attn_fwd joins, a caller's lists)
+// is read by plain loads behind wait_previous_kernel(), never through the read-only path.
 #include <type_traits>
 
 #include "sa_device.cuh"
@@ -94,8 +96,8 @@ struct Part {
   const int32_t* list;
   __device__ __forceinline__ void open(const Args& a, int it, int64_t skip, int left) {
     item = __shfl_sync(0xFFFFFFFFu, it, 0);
-    const int full = __ldg(a.t.tcnt + 2 * static_cast<int64_t>(item));
-    const int all = full + __ldg(a.t.tcnt + 2 * static_cast<int64_t>(item) + 1);
+    const int full = a.t.tcnt[2 * static_cast<int64_t>(item)];
+    const int all = full + a.t.tcnt[2 * static_cast<int64_t>(item) + 1];
     n_full = __shfl_sync(0xFFFFFFFFu, full, 0);
     n = __shfl_sync(0xFFFFFFFFu, all, 0);
     list = a.t.tidx + static_cast<int64_t>(item) * a.t.Tm;
@@ -127,12 +129,12 @@ struct Tiles {
   int base, mine;
   __device__ __forceinline__ void start(const Part& p, int lane) {
     base = p.k;
-    mine = base + lane < p.n ? __ldg(p.list + base + lane) : 0;
+    mine = base + lane < p.n ? p.list[base + lane] : 0;
   }
   __device__ __forceinline__ int at(const Part& p, int k, int lane) {
     if (k - base == 32) {
       base = k;
-      mine = base + lane < p.n ? __ldg(p.list + base + lane) : 0;
+      mine = base + lane < p.n ? p.list[base + lane] : 0;
     }
     return __shfl_sync(0xFFFFFFFFu, mine, k - base);
   }
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const int i = tile * 128 + 32 * y + lane;
-          l[x][y] = i < a.Sq ? __ldg(row + i) : -INFINITY;
+          l[x][y] = i < a.Sq ? row[i] : -INFINITY;
         }
         if (++hh == ka.G) {
           hh = 0;
@@ -427,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t at = f.at;       // where the item begins on the line
     int64_t skip = f.skip;   // units of the item before this CTA's
     if (n_iter > 0 && p.item != f.item) {
-      at += length_of(ka, __ldg(a.tcnt + 2 * static_cast<int64_t>(f.item)) +
-                              __ldg(a.tcnt + 2 * static_cast<int64_t>(f.item) + 1));
+      const int32_t* n = a.tcnt + 2 * static_cast<int64_t>(f.item);
+      at += length_of(ka, n[0] + n[1]);
       skip = 0;
     }
     while (it < n_iter) {
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.mode == SA_MODE_BLOCK && a.bs == 64 && key_ok) {
             const int64_t mb = q0 / 64;
             if (!(mb < a.Mb &&
-                  __ldg(a.mask + (static_cast<int64_t>(bg) * a.Mb + mb) * a.Nb + j / 64) != 0))
+                  a.mask[(static_cast<int64_t>(bg) * a.Mb + mb) * a.Nb + j / 64] != 0))
               cm = 0u;
           } else if (a.mode == SA_MODE_INDEX) {
             // lane L loads the presence word of query q0 + L over this warp's 32 keys; the
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int w = nt * 4 + quarter;
             const uint32_t bits =
                 (i < a.Sq && w < a.W)
-                    ? __ldg(a.bitmap + (static_cast<int64_t>(bg) * a.Sq + i) * a.W + w)
+                    ? a.bitmap[(static_cast<int64_t>(bg) * a.Sq + i) * a.W + w]
                     : 0u;
             cm &= warp_transpose32(bits, lane);
           }
@@ -596,9 +598,10 @@ __global__ void __launch_bounds__(128) key_weights_join_kernel(const Args ka) {
     return;
   }
   const int i0 = (c - ka.C) * 32;
-  for (int i = i0; i < min(i0 + 32, ka.items); ++i)
-    if (__ldg(a.tcnt + 2 * static_cast<int64_t>(i)) + __ldg(a.tcnt + 2 * static_cast<int64_t>(i) + 1) == 0)
-      store(i, 0.f);
+  for (int i = i0; i < min(i0 + 32, ka.items); ++i) {
+    const int32_t* n = a.tcnt + 2 * static_cast<int64_t>(i);
+    if (n[0] + n[1] == 0) store(i, 0.f);
+  }
 }
 
 template <int DQK>

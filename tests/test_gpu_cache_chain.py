@@ -85,3 +85,32 @@ def test_key_weights_then_evict(Sq):
         got = chain(q, lambda: None)
         want = chain(q, torch.cuda.synchronize)
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("D", [D64, D128, D192, D256], ids=str)
+def test_key_weights_of_the_token_that_cache_attn_fwd_decoded(D):
+    """cache_attn_fwd's lse is read by sparse_attn_key_weights as soon as it is joined; the weights
+    are those that cache_attn_fwd gives itself, to the rounding of both."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    B, S, HK, HQ = 3, 1027, 2, 8
+    g, k, v, _, _ = _caches(B, S, HK, D, seed=29)
+    lens = torch.full((B,), S, dtype=torch.int32, device="cuda")
+    lists = sa.block_mask_to_block_sparse(None, B, HK, 1, S)
+    qs = [torch.randn((B, 1, HQ, D[0]), generator=g, device="cuda").bfloat16() for _ in range(20)]
+    torch.cuda.synchronize()
+    got = []
+    for q in qs:
+        _, lse = sa.cache_attn_fwd(q, k, v, lens)
+        got.append(sa.sparse_attn_key_weights(q, k, lse, lists))
+    torch.cuda.synchronize()
+    for q, w in zip(qs, got):
+        o, lse, own = sa.cache_attn_fwd(q, k, v, lens, with_weights=True)
+        torch.cuda.synchronize()
+        assert torch.equal(w, sa.sparse_attn_key_weights(q, k, lse, lists))
+        # two computations of a score less its lse, each off by twice score_bound of cache_ref.py
+        # (s: the largest sum of a score's terms), two exponentials and the additions of four heads
+        s = (D[0] ** -0.5 * torch.einsum("bqhd,bsgd->bhgs", q.double().abs(),
+                                         k.double().abs())).max().item()
+        rel = 2 * ((D[0] + 8) * 2.0 ** -24 * s + 2.0 ** -20 + 2.0 ** -22 * s) + 2.0 ** -20
+        assert ((w - own).abs().double() <= 2 * rel * own.double()).all()
