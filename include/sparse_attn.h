@@ -377,9 +377,12 @@ typedef struct cache_attn_params {
  *   sequence's own keys j < lens[b] (when weights_out is given), and = weights[b][hk][j]
  *   (0 without `weights`) behind them.
  * The new token's own key and value are stored in the cache, and counted in lens, before
- * the call.  Rows of the caches behind lens[b] are never used, whatever they hold.  A
- * sequence with no key at all (lens[b] == 0, P == 0) gets o = 0, lse = -inf.  A length
- * outside [0, S] is clamped to that range and sets SA_STATUS_INDEX in *dev_status.
+ * the call.  Rows of the caches behind lens[b] are never used, whatever they hold.  Of the
+ * rows used, an infinite value makes its column of o infinite whatever its weight (NaN where
+ * both infinities or a NaN meet; such a column costs a second look at its values), a score of
+ * -inf takes no part, and one of +inf or NaN leaves NaN in its row's o and lse.  A sequence
+ * with no key at all (lens[b] == 0, P == 0) gets o = 0, lse = -inf.  A length outside [0, S] is
+ * clamped to that range and sets SA_STATUS_INDEX in *dev_status.
  * Supported: HQ / HK <= 128, B and HQ <= 65535 (SA_ERR_UNSUPPORTED above).  `workspace` is
  * device memory of at least cache_attn_workspace_size() bytes, 16-byte aligned, not
  * initialised, used by this call alone until its work has run.  Results do not depend on the

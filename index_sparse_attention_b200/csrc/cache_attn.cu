@@ -577,6 +577,65 @@ __global__ void __launch_bounds__(352, 1)
 // ------------------------------------------------------------------------------------
 constexpr int kJoin = 128;
 
+// An infinite value v_jd makes a row's column d infinite, however small p_j is, but the products
+// of the parts hold 0 x infinity = NaN too: a row's copies meet every key of a tile, with P = 0
+// where another copy has it, and P or a rescaling underflows.  So where a column is NaN though the
+// row's probabilities are numbers, the largest and the smallest of its values decide: NaN with a
+// NaN or both infinities among them, or with none (sums of finite values that overflowed).
+// A warp looks at 32 columns of one (sequence, KV head), whose rows of the caches and of the
+// prefix begin at `own` and `shared`; this lane's answer is for column 8 (lane % 4) + lane / 4.
+// Rarely called (never on finite values), so it is kept short, with 16 keys in flight: eight loads
+// per lane instead of two cost every call registers and instruction fetches (8 sequences over a
+// prefix of 4097 at D=256 34.0 us against 32.9, 4096 sequences of 128 keys 692 against 659).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+__device__ __forceinline__ float column_of_specials(const __nv_bfloat16* own, int64_t n_own,
+                                                    const __nv_bfloat16* shared, int64_t n_shared,
+                                                    int64_t pitch) {
+  const int lane = threadIdx.x & 31;
+  uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};  // pairs of bf16
+#pragma unroll 1
+  for (int64_t j0 = lane >> 2; j0 < n_shared + n_own; j0 += 16) {
+    uint4 x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t j = j0 + 8 * e;
+      const __nv_bfloat16* v = j < n_shared ? shared + j * pitch : own + (j - n_shared) * pitch;
+      x[e] = j < n_shared + n_own ? __ldcg(reinterpret_cast<const uint4*>(v + 8 * (lane & 3)))
+                                  : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hi[i] = max_bf16x2(hi[i], y[i]);
+        lo[i] = min_bf16x2(lo[i], y[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      hi[i] = max_bf16x2(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], d));
+      lo[i] = min_bf16x2(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], d));
+    }
+  const int i = lane >> 3;
+  const uint32_t hw = i < 2 ? (i ? hi[1] : hi[0]) : (i < 3 ? hi[2] : hi[3]);
+  const uint32_t lw = i < 2 ? (i ? lo[1] : lo[0]) : (i < 3 ? lo[2] : lo[3]);
+  const float p = __uint_as_float(lane & 4 ? hw & 0xFFFF0000u : hw << 16);
+  const float m = __uint_as_float(lane & 4 ? lw & 0xFFFF0000u : lw << 16);
+  // (infinity - infinity, and a sum of finite values, are left NaN)
+  return p == INFINITY || m == -INFINITY ? p + m : __uint_as_float(0x7FC00000u);
+}
+
 template <int DV, int kW>
 __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
   constexpr int kD = DV / 32, kRows = 4 / kW;
@@ -648,11 +707,13 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
 #pragma unroll
   for (int e = 0; e < kD; ++e) acc[e] = 0.f;
   for (int i0 = 0; i0 < n; i0 += 32) {
-    float f = 0.f;  // of part i0 + lane (0: a part without keys)
+    // of part i0 + lane (0: a part without keys; else a normal number, which an infinity in the
+    // part's output outlasts)
+    float f = 0.f;
     if (i0 + lane < n) {
       const float2 v = *ml_of(i0 + lane);
       if (v.y != 0.f) {
-        f = ex2(v.x - me);
+        f = ex2(fmaxf(v.x - me, -126.f));
         l += v.y * f;
       }
     }
@@ -681,6 +742,7 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  bool bad = false;
   if constexpr (kW > 1) {
 #pragma unroll
     for (int e = 0; e < kD; ++e) sh_o[warp][e * 32 + lane] = acc[e];
@@ -689,11 +751,29 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
       float o = 0.f;
 #pragma unroll
       for (int x = 0; x < kW; ++x) o += sh_o[x][d];
-      a.o[row * DV + d] = __float2bfloat16(o * inv);
+      o *= inv;
+      bad |= o != o;
+      a.o[row * DV + d] = __float2bfloat16(o);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < kD; ++e) a.o[row * DV + e * 32 + lane] = __float2bfloat16(acc[e] * inv);
+    for (int e = 0; e < kD; ++e) {
+      const float o = acc[e] * inv;
+      bad |= o != o;
+      a.o[row * DV + e * 32 + lane] = __float2bfloat16(o);
+    }
+  }
+  if (__any_sync(0xFFFFFFFFu, bad) && l == l) {
+    const int64_t pitch = static_cast<int64_t>(a.HK) * DV;
+    __syncwarp();  // (the warp's own stores are read back)
+#pragma unroll 1
+    for (int d = warp * 32; d < DV; d += kW * 32) {
+      const int64_t at = static_cast<int64_t>(hk) * DV + d;
+      const float x = column_of_specials(a.v + b * a.S * pitch + at, clamped_len(a, b), a.vp + at,
+                                         a.P, pitch);
+      __nv_bfloat16* o = a.o + row * DV + d + 8 * (lane & 3) + (lane >> 2);
+      if (__hisnan(*o)) *o = __float2bfloat16(x);
+    }
   }
   if (lane == 0 && warp == 0)
     a.lse[row] = l == 0.f ? -INFINITY : (me + __log2f(l)) * 0.69314718055994531f;

@@ -1,8 +1,10 @@
 """cache_attn_fwd where its warps, its workspace and its arithmetic have their edges: row maxima
-that move by turns in either half of a tile, workspaces at every alignment that is allowed."""
+that move by turns in either half of a tile, workspaces at every alignment that is allowed,
+infinities and NaN among the keys and values that a row sees."""
 import numpy as np
 import pytest
 
+import cache_ref as R
 from index_sparse_attention_b200 import inputs as I
 
 from test_gpu_cache_attn import Case, D64, D128, D192, D256, _compare, _gpu
@@ -87,3 +89,90 @@ def test_a_workspace_of_exact_size_at_any_16_byte_boundary(D, shift):
     got = sa.cache_attn_fwd(**c.g, weights=w, with_weights=True, workspace=pool[at:at + need])
     _compare(got, *c.reference())
     assert (pool[:at] == 0xA5).all() and (pool[at + need:] == 0xA5).all()
+
+
+SPECIAL = {
+    "copies_of_rows_d64": dict(lens=[700, 130], HQ=4, HK=2, D=D64),
+    "copies_of_rows_d128": dict(lens=[700, 130], HQ=4, HK=2, D=D128, P=200),
+    "copies_of_rows_d192": dict(lens=[700, 130], HQ=4, HK=2, D=D192, P=200),
+    "copies_of_rows_d256": dict(lens=[700, 130], HQ=4, HK=2, D=D256, P=200),
+    "whole_buffers_d64": dict(lens=[700, 130], HQ=80, HK=2, D=D64, P=200),
+    "whole_buffers_d128": dict(lens=[700, 130], HQ=80, HK=2, D=D128, P=200),
+    "whole_buffers_d192": dict(lens=[700, 130], HQ=80, HK=2, D=D192, P=200),
+    "whole_buffers_d256": dict(lens=[700, 130], HQ=80, HK=2, D=D256, P=200),
+    "a_warp_per_row_d64": dict(lens=[60 + i % 90 for i in range(520)], HQ=4, HK=2, D=D64, P=40),
+    "a_warp_per_row_d128": dict(lens=[60 + i % 90 for i in range(520)], HQ=4, HK=2, D=D128),
+    "a_warp_per_row_d192": dict(lens=[60 + i % 90 for i in range(520)], HQ=4, HK=2, D=D192, P=40),
+    "a_warp_per_row_d256": dict(lens=[60 + i % 90 for i in range(520)], HQ=4, HK=2, D=D256),
+}
+
+
+@pytest.mark.parametrize("name", SPECIAL)
+def test_infinite_values_that_a_row_sees(name):
+    """o is infinite in the columns where a value is, NaN where one is NaN or both infinities
+    meet, and right everywhere else; lse and weights know nothing of it.  Behind the lengths lie
+    infinities and NaN as well."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    c = Case(seed=540, **SPECIAL[name])
+    c.poison()
+    inf, nan = float("inf"), float("nan")
+    B, G, Dv = len(c.lens), c.q.shape[2] // c.k.shape[2], c.v.shape[3]
+    want = np.zeros((B, 1, c.q.shape[2], Dv))  # what is added to a finite column
+
+    def put(b, j, g, d, x):
+        c.g["v_cache"][b, j, g, d] = x
+        c.v[b, j, g, d] = 0.0
+        with np.errstate(invalid="ignore"):  # (both infinities: NaN)
+            want[b, 0, g * G:(g + 1) * G, d] += x
+
+    put(0, 0, 0, 0, inf)                          # the first key, the first column
+    put(0, int(c.lens[0]) - 1, 0, Dv - 1, -inf)   # the last ones
+    for j, x in ((17, inf), (57, -inf)):          # both infinities, in different quarters of a tile
+        put(0, j, 1, 5, x)
+    for j in (3, 40, 59):                         # one infinity several times
+        put(0, j, 1, Dv // 2 + 1, -inf)
+    put(0, 33, 1, 9, nan)
+    put(0, 34, 1, 9, inf)
+    put(B - 1, 20, 1, 40, inf)
+    if c.vp is not None:                          # every sequence sees the prefix
+        for j, d, x in ((len(c.vp) - 1, 2, inf), (0, 3, -inf)):
+            c.g["v_prefix"][j, 0, d] = x
+            c.vp[j, 0, d] = 0.0
+            want[:, 0, :G, d] += x
+    w = torch.from_numpy(c.w).cuda()
+    got = sa.cache_attn_fwd(**c.g, weights=w, with_weights=True)
+    (o, *rest), (tol, *rest_tol) = c.reference()
+    for what, x, r, t in zip(("lse", "weights"), got[1:], rest, rest_tol):
+        assert (np.abs(x.double().cpu().numpy() - r) <= t).all(), what
+    x, even = got[0].double().cpu().numpy(), want == 0
+    assert (np.abs(x[even] - o[even]) <= tol[even]).all()
+    assert np.array_equal(x[~even], want[~even], equal_nan=True)
+
+
+@pytest.mark.parametrize("name", [n for n in SPECIAL if "d128" in n or "d256" in n])
+def test_infinite_keys_that_a_row_sees(name):
+    """A key with an infinite component: a score of -inf takes no part, one of +inf leaves NaN in
+    its rows' outputs and no others."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    c = Case(seed=560, **SPECIAL[name])
+    G = c.q.shape[2] // c.k.shape[2]
+    c.g["k_cache"][0, 33, 1, 3] = float("inf")
+    up = c.q[0, 0, G:, 3] > 0
+    assert up.any() and not up.all() and (c.q[0, 0, G:, 3] != 0).all()
+    o, lse, w = (t.double().cpu().numpy() for t in sa.cache_attn_fwd(**c.g, with_weights=True))
+    assert np.isnan(o[0, 0, G:][up]).all() and not np.isfinite(lse[0, G:, 0][up]).any()
+    for h in np.flatnonzero(~up):
+        q = c.q[0, 0, G + h]
+        keys = np.delete(c.k[0, :c.lens[0], 1], 33, 0)
+        vals = np.delete(c.v[0, :c.lens[0], 1], 33, 0)
+        if c.kp is not None:
+            keys = np.concatenate([c.kp[:, 1], keys])
+            vals = np.concatenate([c.vp[:, 1], vals])
+        ro, rl, _, pv = R.softmax_rows(q[None], keys, vals, c.scale)
+        ds = R.score_bound(q[None], keys, c.scale)
+        assert abs(lse[0, G + h, 0] - rl[0]) <= ds
+        tol = 2.0 ** -8 * (pv + np.abs(ro)) + (2 * ds + 2.0 ** -20) * pv
+        assert (np.abs(o[0, 0, G + h] - ro[0]) <= tol[0]).all()
+    assert np.isfinite(o[0, 0, :G]).all() and np.isfinite(o[1:]).all() and np.isfinite(w[1:]).all()
