@@ -28,23 +28,59 @@ std::atomic<int> g_bwd_form{SA_BWD_FORM_AUTO};  // read by launch_bwd (bwd.cu)
 
 namespace {
 
+// A driver function in the form that CUDA `version` gave it (null when there is no driver).
+// Without a version a newer form of the name, with other arguments, could come back.
+template <class F>
+F driver_fn(const char* name, unsigned version) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<F>(p);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
+  static const auto fn =
+      driver_fn<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled", 12000);
   return fn;
+}
+
+// Whether a stream under capture belongs to the current device.  It cannot be asked for its device
+// (the query ends the capture), but for its context: that has to be the current one, or, where
+// this thread has none yet, one of the device.
+int check_capturing_stream(cudaStream_t st, int device) {
+  static const auto of_stream = driver_fn<PFN_cuStreamGetCtx_v9020>("cuStreamGetCtx", 9020);
+  static const auto current = driver_fn<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
+  static const auto push = driver_fn<PFN_cuCtxPushCurrent_v4000>("cuCtxPushCurrent", 4000);
+  static const auto pop = driver_fn<PFN_cuCtxPopCurrent_v4000>("cuCtxPopCurrent", 4000);
+  static const auto get_device = driver_fn<PFN_cuCtxGetDevice_v2000>("cuCtxGetDevice", 2000);
+  if (!of_stream || !current || !push || !pop || !get_device) return SA_ERR_CUDA;
+  CUcontext its = nullptr, ours = nullptr;
+  if (of_stream(st, &its) != CUDA_SUCCESS || current(&ours) != CUDA_SUCCESS) return SA_ERR_CUDA;
+  if (ours) return its == ours ? SA_OK : SA_ERR_DEVICE;
+  CUdevice d = -1;
+  if (push(its) != CUDA_SUCCESS) return SA_ERR_CUDA;
+  const bool found = get_device(&d) == CUDA_SUCCESS;
+  if (pop(&its) != CUDA_SUCCESS || !found) return SA_ERR_CUDA;
+  return d == device ? SA_OK : SA_ERR_DEVICE;
 }
 
 }  // namespace
 
 namespace sa {
+int check_stream_device(cudaStream_t st) {
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) return SA_ERR_CUDA;
+  if (st == nullptr || st == cudaStreamLegacy || st == cudaStreamPerThread) return SA_OK;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return SA_ERR_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) return check_capturing_stream(st, cur);
+  int sd = -1;
+  if (cudaStreamGetDevice(st, &sd) != cudaSuccess) return SA_ERR_CUDA;
+  return sd == cur ? SA_OK : SA_ERR_DEVICE;
+}
+
 bool make_map(CUtensorMap* m, const void* base, int D, int64_t S, int H, int B, int box_rows,
               int box_heads) {
   auto fn = encode_fn();

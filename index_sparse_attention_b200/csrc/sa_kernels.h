@@ -122,19 +122,7 @@ int fill_args(const sparse_attn_params* p, AttnArgs* a, bool backward);
 // Every kernel is launched on the current device.  A stream created on another device
 // is refused with SA_ERR_DEVICE before anything is enqueued (the legacy and per-thread
 // default streams always belong to the current device).
-inline int check_stream_device(cudaStream_t st) {
-  int cur = -1;
-  if (cudaGetDevice(&cur) != cudaSuccess) return SA_ERR_CUDA;
-  if (st == nullptr || st == cudaStreamLegacy || st == cudaStreamPerThread) return SA_OK;
-  // A stream that is being captured cannot be asked for its device (the query would end the
-  // capture); a launch into a capture of another device's stream fails by itself.
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone)
-    return SA_OK;
-  int sd = -1;
-  if (cudaStreamGetDevice(st, &sd) != cudaSuccess) return SA_ERR_CUDA;
-  return sd == cur ? SA_OK : SA_ERR_DEVICE;
-}
+int check_stream_device(cudaStream_t st);
 
 int launch_fwd(const AttnArgs& a, const TensorMaps& m, cudaStream_t st);
 int launch_bwd(const AttnArgs& a, const TensorMaps& m, cudaStream_t st);
