@@ -46,6 +46,7 @@ constexpr int kGroups = 4;                        // epilogue warpgroups
 constexpr int kFeed = 2 + 4 * kGroups;            // the feeding warp
 constexpr int kThreads = 32 * (kFeed + 1);
 constexpr int kMaxCtas = 256;
+constexpr int kNoLse = 1 << 30;  // added to a unit's list entry: some of its queries have no lse
 
 template <int DQK>
 struct Cfg {
@@ -364,7 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kFeed) {
     // ---------------------------------------------------------------- feeding warp
     // Four units at a time: their query tiles, list entries and lse values (in log2 units)
-    // into the slots; a row past Sq, or one that saw no key, adds nothing: exp2(-inf).
+    // into the slots.  A row past Sq, or one that saw no key, adds nothing, whatever it holds:
+    // exp2(s - inf) is 0 only for a score s that is a number below infinity, which rows of zeros
+    // past Sq do not have with an infinite key, nor a caller's padded rows with anything in them.
+    // So a unit with such rows is marked in its list entry, which makes it a masked one, with a
+    // mask of its own (index mode's costs 5% more time where every ragged tile is marked; the
+    // schedule of the whole loop changes by as much with where the mark is made and used).
     float* lse_s = reinterpret_cast<float*>(smem + C::kLOff);
     int2* desc = reinterpret_cast<int2*>(smem + C::kDOff);
     bool ok = true;
@@ -374,11 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; ok && it < n_iter; it += 4) {
       float l[4][4];
       int2 d[4];
+      int bits = 0;  // which units are masked by presence words, in which rows past Sq are 0
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         if (it + x >= n_iter) break;
         const int tile = tiles.at(p, k, lane);
         d[x] = make_int2(tile, k);
+        bits |= (a.mode == SA_MODE_INDEX && k >= p.n_full) << x;
         const float* row = a.lse + (static_cast<int64_t>(p.b) * a.HQ + p.h0 + hh) * a.Sq;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -407,6 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int y = 0; y < 4; ++y)
           lse_s[st * 128 + 32 * y + lane] =
               l[x][y] == -INFINITY ? -INFINITY : l[x][y] * -1.4426950408889634f;
+        bool none = false;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          none |= l[x][y] == -INFINITY &&
+                  (!(bits & (1 << x)) || d[x].x * 128 + 32 * y + lane < a.Sq);
+        if (__any_sync(0xFFFFFFFFu, none)) d[x].y += kNoLse;
         if (lane == 0) desc[st] = d[x];
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(kBDone + st));
@@ -477,6 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ? a.bitmap[(static_cast<int64_t>(bg) * a.Sq + i) * a.W + w]
                     : 0u;
             cm &= warp_transpose32(bits, lane);
+          }
+          if (d.y >= kNoLse) {  // (this head's own rows)
+            cm &= __ballot_sync(0xFFFFFFFFu, lse_s[st * 128 + 32 * wg + lane] != -INFINITY);
+            cm_k = -1;
           }
         }
         const ulonglong2* ls2 = reinterpret_cast<const ulonglong2*>(lse_s + st * 128 + 32 * wg);
