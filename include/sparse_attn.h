@@ -360,7 +360,7 @@ typedef struct cache_attn_params {
   void *o;                        /* bf16 [B][1][HQ][Dv] */
   float *lse;                     /* fp32 [B][HQ][1], natural log */
   const float *weights;           /* optional fp32 [B][HK][S]: sums so far (NULL: zeros) */
-  float *weights_out;             /* optional fp32 [B][HK][S]; may be `weights` */
+  float *weights_out;             /* optional fp32 [B][HK][S]; `weights` itself or apart from it */
   int32_t B, HQ, HK, Dqk, Dv;
   int64_t S, P;
   float softmax_scale;
@@ -402,7 +402,8 @@ size_t cache_attn_workspace_size(const cache_attn_params *p);
  * (weights NULL: zeros).  Takes the q, k, softmax_scale, sparse lists (every mode) and
  * dev_status of `p` and the lse that sparse_attn_fwd wrote; v, o and the gradient fields are
  * not read (Dv still selects the head-dim pair).  A query whose lse is -inf adds nothing.
- *   weights, weights_out  fp32 [B][HK][Sk]; may be the same array.
+ *   weights, weights_out  fp32 [B][HK][Sk]; the same array, or apart (SA_ERR_INVALID where
+ *                         they share a part only, here and in cache_attn_fwd).
  * The sums are taken in a fixed order (two calls give identical bits).  `workspace`: device
  * memory of at least sparse_attn_key_weights_workspace_size() bytes,
  * 16-byte aligned, not initialised, used by this call alone until its work has run.

@@ -462,6 +462,7 @@ def cache_attn_fwd(q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None, soft
         _check("workspace", workspace, torch.uint8, device=dev)
     code = L.cache_attn_fwd(ref, workspace.data_ptr(), workspace.numel(), _stream(dev))
     if code:
+        _require_same_or_apart(weights, weights_out)
         _lib.check("cache_attn_fwd", code)
     return (o, lse) if weights_out is None else (o, lse, weights_out)
 
@@ -505,6 +506,7 @@ def sparse_attn_key_weights(q, k, lse, sparse, softmax_scale=None, weights=None,
     code = L.sparse_attn_key_weights(ref, _addr(weights), weights_out.data_ptr(),
                                      workspace.data_ptr(), workspace.numel(), _stream(dev))
     if code:
+        _require_same_or_apart(weights, weights_out)
         _lib.check("sparse_attn_key_weights", code)
     return weights_out
 
@@ -581,6 +583,14 @@ def cache_evict(k_cache, v_cache, weights, lens, budget, sinks=0, recent=0, k_ou
     if code:
         _lib.check("cache_evict", code)
     return k_out, v_out, weights_out, lens_out, keep
+
+
+def _require_same_or_apart(weights, weights_out):
+    """weights_out is weights itself or shares no memory with it."""
+    if weights is not None and weights_out is not None:
+        step = abs(weights_out.data_ptr() - weights.data_ptr())
+        _require(step == 0 or step >= 4 * weights.numel(),
+                 "weights_out overlaps weights without being the same tensor")
 
 
 def _require_apart(inputs, outputs):

@@ -932,6 +932,9 @@ extern "C" int cache_attn_fwd(const cache_attn_params* p, void* workspace, size_
   if ((p->P > 0) != (p->k_prefix != nullptr) || (p->P > 0) != (p->v_prefix != nullptr))
     return SA_ERR_INVALID;
   if (p->weights && !p->weights_out) return SA_ERR_INVALID;
+  if (partly_overlap(p->weights, static_cast<const float*>(p->weights_out),
+                     static_cast<int64_t>(p->B) * p->HK * p->S))
+    return SA_ERR_INVALID;
   if (!(p->softmax_scale > 0.f)) return SA_ERR_INVALID;
   const void* ptrs[] = {p->q, p->k_cache, p->v_cache, p->k_prefix, p->v_prefix, p->o};
   for (const void* x : ptrs)

@@ -659,6 +659,9 @@ extern "C" int sparse_attn_key_weights(const sparse_attn_params* p, const float*
   int rc = fill_args(&fake, &a.t, false);
   if (rc) return rc;
   if (!weights_out) return SA_ERR_INVALID;
+  if (partly_overlap(weights, static_cast<const float*>(weights_out),
+                     static_cast<int64_t>(p->B) * p->HK * p->Sk))
+    return SA_ERR_INVALID;
   const void* words[] = {p->lse, weights, weights_out, p->dev_status};
   for (const void* x : words)
     if ((reinterpret_cast<uintptr_t>(x) & 3u) != 0) return SA_ERR_ALIGN;

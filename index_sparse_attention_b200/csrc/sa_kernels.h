@@ -119,6 +119,14 @@ bool make_map(CUtensorMap* m, const void* base, int D, int64_t S, int H, int B, 
 // Checks an attention call's parameters and fills the launch arguments from them.
 int fill_args(const sparse_attn_params* p, AttnArgs* a, bool backward);
 
+// Whether two arrays of n elements share memory without being the same array: a kernel that reads
+// one element and writes another of the same index may then read what it has already written.
+template <class T>
+inline bool partly_overlap(const T* a, const T* b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x != y && (x < y ? y - x : x - y) / sizeof(T) < static_cast<uint64_t>(n);
+}
+
 // Every kernel is launched on the current device.  A stream created on another device
 // is refused with SA_ERR_DEVICE before anything is enqueued (the legacy and per-thread
 // default streams always belong to the current device).

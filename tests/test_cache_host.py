@@ -209,3 +209,30 @@ def test_references_agree_with_dense_softmax():
         order = 1 + np.argsort(-wts[0, g, 1:10], kind="stable")[:3]
         assert keep[0, g].tolist() == sorted([0, *order.tolist(), 10, 11])
         assert keep[1, g].tolist() == [0, 1, 2, -1, -1, -1]
+
+
+@pytest.mark.parametrize("step", [4, 4 * (2 * 2 * 100 - 1)])
+def test_weights_that_overlap_in_part_are_refused(lib, step):
+    """Element j of one array is another element of the other: what is read would depend on which
+    thread has written."""
+    for a, b in ((0x100000, 0x100000 + step), (0x100000 + step, 0x100000)):
+        assert call_attn(lib, attn(weights=a, weights_out=b)) == BAD
+        s = _lib.BlockSparseStruct(_lib.SA_MODE_DENSE, 0, 2, 2, 256, 100, 128, 0, 0, None, None,
+                                   0x1000, 0x1000, 0x1000, 0x1000)
+        p = _lib.ParamsStruct(0x1000, 0x1000, None, None, 0x1000, None, None, None, None, 2, 4, 2,
+                              128, 128, 256, 100, 0.125, ctypes.pointer(s), None)
+        assert lib.sparse_attn_key_weights(ctypes.byref(p), a, b, None, 0, None) == BAD
+    # the same array, and arrays that touch, get as far as the workspace
+    for a, b in ((0x100000, 0x100000), (0x100000, 0x100000 + 4 * 400), (0x100000 + 4 * 400, 0x100000)):
+        assert call_attn(lib, attn(weights=a, weights_out=b), None, 0) == _lib.SA_ERR_WORKSPACE
+        assert lib.sparse_attn_key_weights(ctypes.byref(p), a, b, None, 0,
+                                           None) == _lib.SA_ERR_WORKSPACE
+
+
+def test_binding_names_weights_that_overlap_in_part(lib, cuda_check_off, monkeypatch):
+    monkeypatch.setattr(sa, "_stream", lambda device: None)
+    q, k = bf(2, 1, 4, 128), bf(2, 8, 2, 128)
+    lens, pool = torch.zeros(2, dtype=torch.int32), torch.zeros(64)
+    w, out = pool[:32].view(2, 2, 8), pool[16:48].view(2, 2, 8)
+    with pytest.raises(ValueError, match="weights_out overlaps"):
+        sa.cache_attn_fwd(q, k, k, lens, weights=w, weights_out=out)
