@@ -65,6 +65,7 @@ struct Cfg {
   static constexpr int kXOff = kDOff + 4 * 8;             // part sums, [2][kGroups - 1][128]
   static constexpr int kFindOff = kXOff + 2 * (kGroups - 1) * 128 * 4;
   static constexpr int kBarOff = kFindOff + 48 * 8;
+  static constexpr int kReadOff = kBarOff + 256;  // per epilogue warp: units read
   static constexpr int kSmem = kBarOff + 384 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -447,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += length_of(ka, n[0] + n[1]);
       skip = 0;
     }
-    while (it < n_iter) {
+    int left = n_iter;
+    while (left > 0) {
       // ------------------------------------------------------------ one part: units of an item
       const int64_t all = static_cast<int64_t>(p.n) * ka.G;
       const int it_end = it + p.units;
@@ -456,13 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool key_ok = j < a.Sk;
       float total = 0.f;
       int cm_k = -1;
-      for (; it < it_end; ++it) {
+      // (a warp whose wait gave up goes from part to part without work, so that the groups meet)
+      for (; ok && it < it_end; ++it) {
         const int st = it % C::kStages;
-        // (a warp whose wait gave up goes on without work, so that the groups still meet)
-        if (ok)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBDone + st), (it / C::kStages) & 1, ctl,
-                                                 a.status, a.wait_limit_ns));
-        if (!ok) continue;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(BAR(kBDone + st), (it / C::kStages) & 1, ctl,
+                                               a.status, a.wait_limit_ns));
+        if (!ok) break;
         tc_fence_after();
         uint32_t s[32];
         tmem_ld32(tl + st * 128 + 32 * wg, s);
@@ -558,8 +559,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += length_of(ka, p.n);
       skip = 0;
       ++part;
-      if (it < n_iter) p.next(ka, n_iter - it);
+      left -= p.units;
+      if (left > 0) p.next(ka, left);
     }
+    // (for the abort path: the units whose S buffers this warp has read)
+    if (lane == 0) reinterpret_cast<int*>(smem + C::kReadOff)[warp - 2] = it;
     if (n_iter > 0 && wg == 0 && r == 0 && !cut_here) ka.fix[cta] = make_int2(-1, 0);
   }
 
@@ -571,10 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
       for (int k = max(0, issued_k - C::kKStages); k < issued_k; ++k)
         mbar_wait_limited(BAR(kBKF + k % C::kKStages), (k / C::kKStages) & 1);
-      // (a Q tile's barrier also counts its S buffer's readers, who may have left: its bytes
-      // are given 50 us instead, against a few for a load)
-      const uint64_t t0 = globaltimer_ns();
-      while (issued_q > 0 && globaltimer_ns() - t0 < 50000) __nanosleep(1000);
+      // a Q tile's barrier also counts the readers of the unit that had its S buffer before:
+      // for those that gave up there, the arrival is made here
+      const int* read_s = reinterpret_cast<const int*>(smem + C::kReadOff);
+      for (int it = max(0, issued_q - C::kStages); it < issued_q; ++it) {
+        const uint32_t bar = BAR(kBFull + it % C::kStages);
+        for (int w = 0; w < 4 * kGroups; ++w)
+          if (it >= C::kStages && read_s[w] <= it - C::kStages) mbar_arrive(bar);
+        mbar_wait_limited(bar, (it / C::kStages) & 1);
+      }
     }
     if (warp == 1) {
       tc_fence_after();

@@ -68,3 +68,29 @@ def test_a_key_that_no_query_weighs(w):
     allowed[..., 5] = False
     ref, tol = R.key_weights(bf16_to_f64(g["q"]), k, lse.double().cpu().numpy(), allowed, w.scale)
     _compare(got, ref, tol)
+
+
+@pytest.mark.parametrize("limit", [100, 1000, 3000, 10000, 30000, 100000])
+@pytest.mark.parametrize("w", [CASES[4], CASES[5]], ids=lambda w: w.name)
+def test_a_call_given_up_ends_when_its_copies_have_landed(w, limit):
+    """Whatever state a CTA gives up in, it waits for its own loads and no longer: a wait for an
+    arrival that nobody makes would take the two seconds of its limit."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    inp = I.make_inputs(w, with_grad=False)
+    g = to_gpu(inp)
+    bsp = build_lists(inp, g)
+    _, lse = sa.sparse_attn_fwd(g["q"], g["k"], g["v"], bsp, w.scale)
+    want = sa.sparse_attn_key_weights(g["q"], g["k"], lse, bsp, w.scale)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    try:
+        sa.sparse_attn_set_wait_limit_ns(limit)
+        start.record()
+        for _ in range(10):
+            sa.sparse_attn_key_weights(g["q"], g["k"], lse, bsp, w.scale)
+        end.record()
+        torch.cuda.synchronize()
+    finally:
+        sa.sparse_attn_set_wait_limit_ns(0)
+    assert start.elapsed_time(end) < 500
+    assert torch.equal(sa.sparse_attn_key_weights(g["q"], g["k"], lse, bsp, w.scale), want)
