@@ -217,6 +217,9 @@ __global__ void __launch_bounds__(352, 1)
         if (!warp_wait(BAR(kBVE + it % C::kVStages), (it / C::kVStages) & 1, ctl, a.status,
                        a.wait_limit_ns))
           break;
+    // (P V's own barrier, which the softmax warps wait for only where they rescale)
+    if (issued_v == n_iter && n_iter > 0)
+      warp_wait(BAR(kBOD), (n_iter - 1) & 1, ctl, a.status, a.wait_limit_ns);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc_s = idesc_bf16(128, kN, 0, 0);

@@ -114,3 +114,54 @@ def test_key_weights_of_the_token_that_cache_attn_fwd_decoded(D):
                                          k.double().abs())).max().item()
         rel = 2 * ((D[0] + 8) * 2.0 ** -24 * s + 2.0 ** -20 + 2.0 ** -22 * s) + 2.0 ** -20
         assert ((w - own).abs().double() <= 2 * rel * own.double()).all()
+
+
+def test_all_calls_in_one_captured_graph_with_branches():
+    """Forward, key weights, two decodes at once, evictions one behind another, with other kernels
+    and branches that join between them: replays give what the same calls gave uncaptured."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    B, S, HQ, HK = 3, 700, 8, 2
+    g, k, v, _, _ = _caches(B, S, HK, D128, seed=39)
+    lens = torch.full((B,), S, dtype=torch.int32, device="cuda")
+    q1 = torch.randn((B, 1, HQ, 128), generator=g, device="cuda").bfloat16()
+    q = torch.randn((B, S, HQ, 128), generator=g, device="cuda").bfloat16()
+    lists = sa.block_mask_to_block_sparse(None, B, HK, S, S)
+
+    def body(side):
+        cur = torch.cuda.current_stream()
+
+        def fork(f):
+            side.wait_stream(cur)
+            with torch.cuda.stream(side):
+                return f()
+
+        k2, n = fork(lambda: (k * 1.0, lens.clone()))
+        v2 = v * 1.0
+        cur.wait_stream(side)
+        _, lse = sa.sparse_attn_fwd(q, k2, v2, lists)
+        q2 = fork(lambda: q * 1.0)
+        k3 = k2 * 1.0
+        cur.wait_stream(side)
+        w = sa.sparse_attn_key_weights(q2, k3, lse, lists)
+        a = fork(lambda: sa.cache_attn_fwd(q1, k2, v2, n))
+        b = sa.cache_attn_fwd(q1, k3, v2, n, weights=w, with_weights=True)
+        cur.wait_stream(side)
+        c = sa.cache_evict(k2, v2, b[2], n, 100, sinks=3, recent=5, k_out=torch.zeros_like(k),
+                           v_out=torch.zeros_like(v))
+        d = fork(lambda: sa.cache_evict(*c[:4], 50, k_out=torch.zeros_like(k),
+                                        v_out=torch.zeros_like(v)))
+        cur.wait_stream(side)
+        return [w, *a, *b, *c, *d]
+
+    want = body(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = body(torch.cuda.Stream())
+    for _ in range(10):
+        for x in out:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want))

@@ -176,3 +176,103 @@ def test_infinite_keys_that_a_row_sees(name):
         tol = 2.0 ** -8 * (pv + np.abs(ro)) + (2 * ds + 2.0 ** -20) * pv
         assert (np.abs(o[0, 0, G + h] - ro[0]) <= tol[0]).all()
     assert np.isfinite(o[0, 0, :G]).all() and np.isfinite(o[1:]).all() and np.isfinite(w[1:]).all()
+
+
+@pytest.mark.parametrize("limit", [100, 1000, 3000, 10000, 30000])
+@pytest.mark.parametrize("D", [D64, D128, D192, D256], ids=str)
+def test_a_call_given_up_ends_when_its_copies_have_landed(D, limit):
+    """Whatever state a CTA gives up in, it waits for its own loads and MMAs and no longer: a wait
+    for an arrival that nobody makes would take the two seconds of its limit."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    c = Case([700, 1, 333] * 9, HQ=8, HK=2, D=D, P=4000, seed=580)
+    want = sa.cache_attn_fwd(**c.g, with_weights=True)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    try:
+        sa.sparse_attn_set_wait_limit_ns(limit)
+        start.record()
+        for _ in range(10):
+            sa.cache_attn_fwd(**c.g, with_weights=True)
+        end.record()
+        torch.cuda.synchronize()
+    finally:
+        sa.sparse_attn_set_wait_limit_ns(0)
+    assert start.elapsed_time(end) < 500
+    got = sa.cache_attn_fwd(**c.g, with_weights=True)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_the_most_sequences_and_the_most_heads():
+    """65535 sequences, and 65535 heads of one sequence: the largest sizes that the call takes."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    for B, H, P in ((65535, 1, 0), (65535, 1, 9), (1, 65535, 0), (1, 65535, 2)):
+        S, D = 3, 64
+        q, k, v = (torch.randn(s, generator=g, device="cuda").bfloat16()
+                   for s in ((B, 1, H, D), (B, S, H, D), (B, S, H, D)))
+        kp, vp = (torch.randn((P, H, D), generator=g, device="cuda").bfloat16() for _ in "kv")
+        lens = torch.randint(0, S + 1, (B,), generator=g, device="cuda").int()
+        o, lse, w = sa.cache_attn_fwd(q, k, v, lens, k_prefix=kp if P else None,
+                                      v_prefix=vp if P else None, with_weights=True)
+        s = torch.einsum("bqhd,bshd->bhs", q.double(), k.double()) / 8
+        size = torch.einsum("bqhd,bshd->bhs", q.double().abs(), k.double().abs()).max() / 8
+        live = (torch.arange(S, device="cuda") < lens[:, None])[:, None].expand_as(s)
+        s = s.masked_fill(~live, -float("inf"))
+        vals = v.double().transpose(1, 2)
+        if P:
+            sp = torch.einsum("bqhd,phd->bhp", q.double(), kp.double()) / 8
+            size = max(size, torch.einsum("bqhd,phd->bhp", q.double().abs(), kp.double().abs()).max() / 8)
+            s = torch.cat([sp, s], 2)
+            vals = torch.cat([vp.double().transpose(0, 1).expand(B, H, P, D), vals], 2)
+        ref_lse = s.logsumexp(2)
+        p = torch.where(ref_lse[..., None] == -float("inf"), 0.0, (s - ref_lse[..., None]).exp())
+        ref, mag = (torch.einsum("bhs,bhsd->bhd", p, x) for x in (vals, vals.abs()))
+        # (the bounds of cache_ref.py)
+        ds = (D + 8) * R.U24 * size + 2.0 ** -20 + 2.0 ** -22 * size
+        none = ref_lse == -float("inf")
+        assert torch.equal(lse[..., 0] == -float("inf"), none)
+        assert ((lse[..., 0].double() - ref_lse)[~none].abs() <= ds).all()
+        tol = 2.0 ** -8 * (mag + ref.abs()) + (2 * ds + 2.0 ** -20) * mag + 1e-30
+        assert ((o[:, 0].double() - ref).abs() <= tol).all()
+        own = p[..., P:]
+        assert ((w.double() - own).abs() <= (2 * ds + 2.0 ** -20 + 2 * R.U24) * own).all()
+
+
+def test_rows_at_the_far_end_of_a_cache_of_more_than_2_to_the_32_elements():
+    """The last sequence fills its capacity: every one of its two million keys takes part."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    B, S, HK, HQ, D = 3, 1 << 21, 8, 16, 128
+    free, _ = torch.cuda.mem_get_info()
+    if free < 48 << 30:
+        pytest.skip("needs 48 GB of free device memory")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    q = torch.randn((B, 1, HQ, D), generator=g, device="cuda").bfloat16()
+    k, v = (torch.empty((B, S, HK, D), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    for x in (k, v):
+        x[:2, :512].normal_(generator=g)
+        for at in range(0, S, 1 << 18):
+            x[2, at:at + (1 << 18)].normal_(generator=g)
+    lens = torch.tensor([200, 1, S], dtype=torch.int32, device="cuda")
+    o, lse = sa.cache_attn_fwd(q, k, v, lens)
+    for h in range(HQ):
+        s, size = torch.empty(S, dtype=torch.float64, device="cuda"), 0.0
+        row = q[2, 0, h].double()
+        for at in range(0, S, 1 << 18):
+            keys = k[2, at:at + (1 << 18), h // 2].double()
+            s[at:at + (1 << 18)] = keys @ row * D ** -0.5
+            size = max(size, (keys.abs() @ row.abs()).max().item() * D ** -0.5)
+        ref_lse = s.logsumexp(0)
+        p = (s - ref_lse).exp()
+        ref, mag = (sum(p[at:at + (1 << 18)] @ f(v[2, at:at + (1 << 18), h // 2].double())
+                        for at in range(0, S, 1 << 18)) for f in (lambda x: x, torch.abs))
+        ds = (D + 8) * R.U24 * size + 2.0 ** -20 + 2.0 ** -22 * size
+        # two million terms are added in 148 parts, by tiles of 128: at most 128 + 16384 / 148
+        # additions in a row, and 148 of the parts, each off by 2^-24 of the sum
+        ds += (128 + 16384 / 148 + 148) * R.U24
+        assert abs(lse[2, h, 0].item() - ref_lse.item()) <= ds
+        tol = 2.0 ** -8 * (mag + ref.abs()) + (2 * ds + 2.0 ** -20) * mag
+        assert ((o[2, 0, h].double() - ref).abs() <= tol).all()
