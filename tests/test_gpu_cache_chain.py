@@ -165,3 +165,37 @@ def test_all_calls_in_one_captured_graph_with_branches():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_the_most_sequences_and_heads_for_weights_and_eviction():
+    """65535 sequences, and 65535 KV heads of one sequence."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    S, D, budget = 5, 64, 3
+    for B, HK in ((65535, 1), (1, 65535)):
+        g, k, v, w, lens = _caches(B, S, HK, D64, seed=49)
+        ko, vo, wo, lo, keep = sa.cache_evict(k, v, w, lens, budget, sinks=1,
+                                              k_out=torch.zeros_like(k), v_out=torch.zeros_like(v))
+        at = torch.arange(S, device="cuda")
+        rank = w.clone()
+        rank[..., 0] = 2.0
+        rank = rank.masked_fill(at >= lens[:, None, None], -1.0)
+        best = rank.sort(dim=-1, descending=True, stable=True).indices[..., :budget]
+        best = torch.where(best < lens[:, None, None], best, S).sort(dim=-1).values
+        assert torch.equal(keep, torch.where(best < S, best, -1).int())
+        assert torch.equal(lo, lens.clamp(max=budget))
+        rows = best.clamp(max=S - 1).transpose(1, 2)[..., None].expand(-1, -1, -1, D)
+        live = (best < S).transpose(1, 2)[..., None]
+        for x, y in ((ko, k), (vo, v)):
+            assert torch.equal(x[:, :budget], torch.where(live, y.gather(1, rows), 0))
+        lists = sa.block_mask_to_block_sparse(None, B, HK, 2, S)
+        q = torch.randn((B, 2, HK, D), generator=g, device="cuda").bfloat16()
+        _, lse = sa.sparse_attn_fwd(q, k, v, lists)
+        got = sa.sparse_attn_key_weights(q, k, lse, lists)
+        s = torch.einsum("bqhd,bshd->bhqs", q.double(), k.double()) / 8
+        size = torch.einsum("bqhd,bshd->bhqs", q.double().abs(), k.double().abs()).max() / 8
+        ref = (s - lse.double()[..., None]).exp().sum(2)
+        # (the bounds of cache_ref.py)
+        rel = 2 * ((D + 8) * 2.0 ** -24 * size + 2.0 ** -20 + 2.0 ** -22 * size)
+        rel = rel + 2.0 ** -22 * lse.abs().max().double() + 130 * 2.0 ** -24
+        assert ((got.double() - ref).abs() <= rel * ref).all()
