@@ -369,8 +369,8 @@ typedef struct cache_attn_params {
 
 /*
  * cache_attn_fwd -- attention of one new token of each sequence b over the P prefix keys
- * (which every sequence of the batch shares and which are read once for all of them) and
- * the first lens[b] keys of its own cache.  Query head h uses KV head h / (HQ / HK):
+ * (which every sequence of the batch shares and which are read once for every
+ * 128 / (HQ / HK) sequences) and the first lens[b] keys of its own cache.  Query head h uses KV head h / (HQ / HK):
  *   s_j = scale * q . k_j over both key sets;  lse = ln sum_j exp(s_j);
  *   o = sum_j exp(s_j - lse) v_j;
  *   weights_out[b][hk][j] = weights[b][hk][j] + sum_{h in group} exp(s_hj - lse_h) for the
@@ -391,8 +391,9 @@ typedef struct cache_attn_params {
 int cache_attn_fwd(const cache_attn_params *p, void *workspace, size_t workspace_bytes,
                    sa_stream_t stream);
 
-/* Bytes of device workspace cache_attn_fwd needs for these shapes (partial outputs and,
- * with weights_out, the scores of the caches' keys); 0 for invalid sizes. */
+/* Bytes of device workspace cache_attn_fwd needs for these shapes: partial outputs and, with
+ * weights_out, the scores of the caches' keys, 4 B HQ S bytes (S rounded up to 128) whatever the
+ * lengths are, since those are on the device; 0 for invalid sizes. */
 size_t cache_attn_workspace_size(const cache_attn_params *p);
 
 /*

@@ -430,9 +430,9 @@ def cache_attn_fwd(q, k_cache, v_cache, lens, k_prefix=None, v_prefix=None, soft
                    weights=None, with_weights=False, weights_out=None, o=None, lse=None,
                    workspace=None, dev_status=None):
     """O [B,1,HQ,Dv] (bf16) and LSE [B,HQ,1] (fp32) of one new token per sequence over the
-    prefix k_prefix / v_prefix [P,HK,D] that the batch shares (read once for all sequences)
-    and the first lens[b] (int32 [B]) keys of each sequence's cache k_cache / v_cache
-    [B,S,HK,D].
+    prefix k_prefix / v_prefix [P,HK,D] that the batch shares (read once for every
+    128 / (HQ / HK) sequences) and the first lens[b] (int32 [B]) keys of each sequence's
+    cache k_cache / v_cache [B,S,HK,D].
 
     With ``with_weights`` (or a ``weights_out``) also weights_out [B,HK,S] (fp32):
     ``weights`` (zeros when omitted) plus the attention weight that each of the sequence's

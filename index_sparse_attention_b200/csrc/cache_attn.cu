@@ -16,17 +16,23 @@
 //   warps 2-9  softmax, two warps per TMEM lane quarter: scores, running maximum and sum, P (bf16)
 //              over S, the part's end.
 // A prefix part holds the query rows of up to 128 / group sequences (box {64, sequences, group} of
-// one TMA load), so a prefix tile is read once for all of them; a cache part holds the group's
-// rows.  An MMA has 128 rows: parts of up to 32 rows load their Q into all four lane quarters, and
-// each quarter's copy takes a quarter of the tile's keys (P is 0 elsewhere), so that all eight
-// softmax warps share the exponentials; the copies are added when the part ends.
+// one TMA load), a row tile, so a prefix tile is read once for all of them.  More sequences make
+// more row tiles, each with its own pass over the prefix, and one that the L2 does not hold from
+// pass to pass comes from HBM each time (64 sequences of 4 heads a group over 32768 keys: two
+// passes, 134 of 1084 MB read).  A cache part holds the group's rows.
+// An MMA has 128 rows: parts of up to 32 rows load their Q into all four lane quarters, and each
+// quarter's copy takes a quarter of the tile's keys (P is 0 elsewhere), so that all eight softmax
+// warps share the exponentials; the copies are added when the part ends.
 // P is rounded to bf16 for the MMA, as the forward does (its sum is taken before in fp32).  The
 // running maximum moves only when a row's exceeds it by 8 (factors up to 2^8 in P, O and l).
 // What bounds it: HBM where the caches are long (64 sequences of 4096 keys, 8 KV heads, D=128:
-// 165 us, 6.5 TB/s, the copy bandwidth measured on this GPU); the softmax warps' chain on prefix
+// 164 us, 6.5 TB/s, the copy bandwidth measured on this GPU); the softmax warps' chain on prefix
 // tiles of many rows (2200 cycles per 128 x 128 tile, of which the exponentials 1200 and the MMAs
-// 1050: 256 sequences over a prefix of 8192, 89 us, 385 TFLOP/s); on short calls the launches,
-// the set-up (lengths, plan, first loads: about 5 us) and the join (3 us).
+// 1050: 256 sequences over a prefix of 8192 alone 56 us, of which a CTA's 28 tiles are 32 and the
+// join of 8192 rows and the set-up the rest); the parts' ends where there are many short caches
+// (one own key for each of those 256 sequences: 92 us in all; 4096 sequences of 128 keys 593 to
+// 670 us on two GPUs, 328 us of bytes); on short calls the launches, the set-up (lengths, plan,
+// first loads: about 5 us) and the join (3 us).
 // Tried without gain: a third K stage; both softmax groups with a tile and an O of their own by
 // turns (2250 cycles a tile again: then the MMA warp's waits and issues bound); an eighth to a
 // half of the exponentials by polynomial (2% on prefix tiles); joining and weighing in one launch
@@ -72,7 +78,7 @@ struct Cfg {
   // (what find_range needs lies there too: every warp is past it when the first part ends)
   static constexpr int kFindOff = kMergeOff;
   static constexpr int kBarOff = kMergeOff + kCols * 1024;
-  static constexpr int kSmem = kBarOff + 272;  // (the swizzled tiles' base is declared 1024-aligned)
+  static constexpr int kSmem = kBarOff + 272;  // (the tiles' base is declared 1024-aligned)
   static constexpr int kThreads = 352;
   static constexpr uint32_t kOCol = 256;  // S / P buffers at columns 0 and 128
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(352, 1)
             xs[r] = l_run + xs[128 + r];
           }
           // (behind it nothing reads the second half of xs; the first half is read by a warp that
-          // meets the writers of the next tile's maxima, the hc == 0 warps, at the merge's barriers)
+          // meets the writers of the next tile's maxima there, the hc == 0 warps, when they merge)
           named_bar_sync(5, 256);
           float mm = -INFINITY;
 #pragma unroll

@@ -20,7 +20,8 @@
 //   copy       16-byte pieces, four rows per thread in flight; by the selection's own CTAs where
 //              they fill the SMs, else by a kernel of its own (writes contiguous over all heads
 //              of a row).  Bound by HBM (each kept row is read and written once): 16 sequences of
-//              8 heads cut from 8191 to 2048 keys, D=128, 52 us in all, 5.1 TB/s of its bytes.
+//              8 heads of 4352 to 8191 keys, one of 511, cut to 2048, D=128, 52 us in all, 5.1 TB/s
+//              of its bytes.
 //              (Asking L2 for the rows that are sure to stay while the selection still runs made
 //              it slower: its warps have no time for that.)
 #include "sa_device.cuh"
@@ -37,7 +38,6 @@ constexpr int kPerThread = kBins / kThreads;
 constexpr int kSlice = 8192;        // keys a CTA takes before the row is spread over more of them
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCtas = 128;       // CTAs that run at once (clusters do not fill every SM)
-constexpr int kSms = 148;
 
 struct Args {
   const uint4 *k, *v;
@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const Args a)
   if constexpr (KPT > 0) {
     float x[kHeld];
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) x[j] = w0 + 32 * j + lane < w1 ? __ldcg(w + w0 + 32 * j + lane) : 0.f;
+    for (int j = 0; j < KPT; ++j)
+      x[j] = w0 + 32 * j + lane < w1 ? __ldcg(w + w0 + 32 * j + lane) : 0.f;
     fill_tails();  // (while the loads are on their way)
 #pragma unroll
     for (int j = 0; j < KPT; ++j) {
@@ -492,12 +493,16 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
   a.sinks = p->sinks;
   a.recent = p->recent;
   a.status = p->dev_status;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SA_ERR_CUDA;
   // rows of a copy CTA: 16, or 4 (one round of loads) where that leaves SMs without work
   const int64_t most = min64(p->budget, p->S);
-  a.rows = (most + 15) / 16 * p->B >= 4 * evict::kSms ? 16 : 4;
+  a.rows = (most + 15) / 16 * p->B >= 4 * sms ? 16 : 4;
   // A row is spread over more CTAs while its slices are long, as long as all clusters run at
-  // once (32 rows of 65536 over 256 CTAs: 56 us; one row's cluster alone takes 20), or until a
-  // slice fits in registers.
+  // once (32 rows of 65536 in all: 115 us over 256 CTAs, 80 over 128), or until a slice fits in
+  // registers.
   a.cluster = 1;
   while (a.cluster < evict::kMaxCluster &&
          (static_cast<int64_t>(a.cluster) * 2 * evict::kSlice < p->S ||
@@ -505,12 +510,13 @@ extern "C" int cache_evict(const cache_evict_params* p, sa_stream_t stream) {
            BH * a.cluster * 2 <= evict::kMaxCtas)))
     a.cluster *= 2;
   // Selection CTAs that fill the SMs copy their own rows (no second launch, and rows that are
-  // selected early are copied while others are not): 64 sequences of 8 heads, 8191 to 2048 keys,
-  // D=128, 191 us against 208, 16 of them 57 against 60.  Few CTAs, or a last wave of them that
-  // leaves SMs idle, would copy with part of the GPU: 2 sequences of 131072 84 us against 77, 20
-  // of 8191 (160 CTAs) 88 against 76.
-  const int64_t ctas = BH * a.cluster, waves = (ctas + evict::kSms - 1) / evict::kSms;
-  a.fused = ctas * 5 >= waves * evict::kSms * 4;
+  // selected early are copied while others are not): 64 full sequences of 8 heads, 8191 to 2048
+  // keys, D=128, 193 us against 209, 16 of them 56 against 61.  Few CTAs, or a last wave of them
+  // that leaves SMs idle, would copy with part of the GPU: 20 of 8191 (160 CTAs) 89 us against 76;
+  // 2 sequences of 131072 (128 CTAs) take 108 either way.  The rule knows the shapes only: one
+  // long sequence among short ones is copied by its own heads' CTAs.
+  const int64_t ctas = BH * a.cluster, waves = (ctas + sms - 1) / sms;
+  a.fused = ctas * 5 >= waves * sms * 4;
   if (BH * a.cluster > 0x7FFFFFFF) return SA_ERR_UNSUPPORTED;
   // keys per thread: a warp's stretch of the longest slice, in whole 32s
   const int64_t slice = ((p->S + a.cluster - 1) / a.cluster + 31) / 32 * 32;

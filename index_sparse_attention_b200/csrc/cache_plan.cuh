@@ -1,8 +1,8 @@
 // cache_plan.cuh -- how cache_attn_fwd splits its work over the CTAs and where the parts meet.
 //
 // The work is a row of key tiles: first the prefix (for every KV head, every tile of query rows,
-// the P keys), then the caches (for every sequence, every KV head, its own keys).  A run of
-// tiles over one key set is a segment.  On a line a tile is as long as it takes (wt_p, wt_c) and
+// the P keys: all of one row tile before the next one's), then the caches (for every sequence,
+// every KV head, its own keys).  A run of tiles over one key set is a segment.  On a line a tile is as long as it takes (wt_p, wt_c) and
 // behind a segment's tiles lies a stretch `we` for what its end takes (reading O, joining its
 // row copies, the next rows' start).  CTA c takes the tiles that begin in [q c, q (c + 1)) of
 // that line (q: its length U over the number of CTAs), so that the CTAs end together whatever
@@ -25,12 +25,14 @@ namespace cache {
 
 constexpr int kMaxCtas = 256;  // bound of C the workspace is sized for
 // From so many (sequence, query head) rows on the join gives a row one warp instead of four
-// (8192 rows of two or three parts: 36 us with four warps, 17 with one).
+// (8192 rows of two or three parts: 36 us with four warps, 17 with one; the whole call for 256
+// sequences of 1024 keys 235 and 205).
 constexpr int kJoinRows = 2048;
 // From so many sequences on such a join takes their places on the line from the workspace; with
 // fewer each warp adds up the lengths itself while the parts are computed (32 heads, D=128, the
-// whole call: 128 sequences of 1024 keys 93.8 us from the workspace, 92.5 without; 256 with a
-// prefix of 8192 92.3 and 93.2; 1024 of 256 keys 200 and 232; 4096 of 128 keys 623 and 1167).
+// whole call: 128 sequences of 1024 keys 97.9 us from the workspace, 97.3 without; 256 of 64 keys
+// with a prefix of 8192 95.5 either way; 1024 of 256 keys 223 and 262; 4096 of 128 keys 593 and
+// 1128).
 constexpr int kLineSeqs = 256;
 
 struct Args {

@@ -23,10 +23,11 @@
 //              lose low bits.
 //   warp 18    feeds the units' lse values and list entries through shared memory.
 // What bounds it: the special-function unit.  A unit's 16384 exponentials take an SM 1024 cycles
-// (its MMAs 512 at head dim 128); measured 1300 to 1400 cycles a unit on long prompts (101 us for
-// the causal prompt B=2 H=16 S=4096 D=128, 684 TFLOP/s of allowed pairs; 103 us for the
-// block-sparse one with 32 / 8 heads, S=8192; 111 us for the index prompt with 32 / 4 heads,
-// S=4001, head dims 192/128).  Tried and slower: a unit per warpgroup (a group stands idle while
+// (its MMAs 512 at head dim 128); measured 1300 to 1400 cycles a unit on long prompts (103 us for
+// the causal prompt B=2 H=16 S=4096 D=128, 667 TFLOP/s of allowed pairs; 106 us for the
+// block-sparse one with 32 / 8 heads, S=8192; 114 to 124 us for the index prompt with 32 / 4
+// heads, S=4001, head dims 192/128: replayed graphs; 107, 115 and 126 us a call made from
+// Python).  Tried and slower: a unit per warpgroup (a group stands idle while
 // its buffer is refilled), eight warps with half a unit each and the next half's TMEM loads in
 // flight (the remaining latency of a unit is shared by fewer warps), an eighth to a half of the
 // exponentials by a polynomial of packed fused multiply-adds (equal to slower: the warps are
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   wait_previous_kernel();
-  // (the join is not let in early: its blocks, waiting, slow the exponentials: 104.8 us for the
-  // causal prompt against 100.6)
+  // (the join is not let in early: its blocks, waiting, slow the exponentials: 109 us for the
+  // causal prompt against 103)
   const Found f = find_range(ka, cta, reinterpret_cast<int64_t*>(smem + C::kFindOff));
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
