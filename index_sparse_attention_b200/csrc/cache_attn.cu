@@ -588,14 +588,14 @@ constexpr int kJoin = 128;
 
 // An infinite value v_jd makes a row's column d infinite, however small p_j is, but the products
 // of the parts hold 0 x infinity = NaN too: a row's copies meet every key of a tile, with P = 0
-// where another copy has it, and P or a rescaling underflows.  So where a column is NaN though the
-// row's probabilities are numbers, the largest and the smallest of its values decide: NaN with a
-// NaN or both infinities among them, or with none (sums of finite values that overflowed).
-// A warp looks at 32 columns of one (sequence, KV head), whose rows of the caches and of the
-// prefix begin at `own` and `shared`; this lane's answer is for column 8 (lane % 4) + lane / 4.
-// Rarely called (never on finite values), so it is kept short, with 16 keys in flight: eight loads
-// per lane instead of two cost every call registers and instruction fetches (8 sequences over a
-// prefix of 4097 at D=256 34.0 us against 32.9, 4096 sequences of 128 keys 692 against 659).
+// where another copy has it, and P or a rescaling underflows.  So where a part's column is NaN
+// though the row's probabilities are numbers, the largest and the smallest of its values decide:
+// this gives their sum where they are no numbers (NaN with a NaN or both infinities), 0 if all
+// are.  A warp looks at 32 columns of n keys, whose rows begin at v; this lane's answer is for
+// column 8 (lane % 4) + lane / 4.  Rarely called (never on finite values), so it is kept
+// short, with 16 keys in flight: eight loads per lane instead of two cost every call registers
+// and instruction fetches (8 sequences over a prefix of 4097 at D=256 34.0 us against 32.9, 4096
+// sequences of 128 keys 692 against 659).
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
   return a;
@@ -604,21 +604,18 @@ __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
   asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
   return a;
 }
-__device__ __forceinline__ float column_of_specials(const __nv_bfloat16* own, int64_t n_own,
-                                                    const __nv_bfloat16* shared, int64_t n_shared,
+__device__ __forceinline__ float column_of_specials(const __nv_bfloat16* v, int64_t n,
                                                     int64_t pitch) {
   const int lane = threadIdx.x & 31;
   uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};  // pairs of bf16
+  v += 8 * (lane & 3);
 #pragma unroll 1
-  for (int64_t j0 = lane >> 2; j0 < n_shared + n_own; j0 += 16) {
+  for (int64_t j = lane >> 2; j < n; j += 16) {
     uint4 x[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int64_t j = j0 + 8 * e;
-      const __nv_bfloat16* v = j < n_shared ? shared + j * pitch : own + (j - n_shared) * pitch;
-      x[e] = j < n_shared + n_own ? __ldcg(reinterpret_cast<const uint4*>(v + 8 * (lane & 3)))
-                                  : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int e = 0; e < 2; ++e)
+      x[e] = j + 8 * e < n ? __ldcg(reinterpret_cast<const uint4*>(v + (j + 8 * e) * pitch))
+                           : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
@@ -631,7 +628,7 @@ __device__ __forceinline__ float column_of_specials(const __nv_bfloat16* own, in
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-#pragma unroll
+#pragma unroll 1
     for (int d = 4; d < 32; d <<= 1) {
       hi[i] = max_bf16x2(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], d));
       lo[i] = min_bf16x2(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], d));
@@ -641,8 +638,7 @@ __device__ __forceinline__ float column_of_specials(const __nv_bfloat16* own, in
   const uint32_t lw = i < 2 ? (i ? lo[1] : lo[0]) : (i < 3 ? lo[2] : lo[3]);
   const float p = __uint_as_float(lane & 4 ? hw & 0xFFFF0000u : hw << 16);
   const float m = __uint_as_float(lane & 4 ? lw & 0xFFFF0000u : lw << 16);
-  // (infinity - infinity, and a sum of finite values, are left NaN)
-  return p == INFINITY || m == -INFINITY ? p + m : __uint_as_float(0x7FC00000u);
+  return (p < INFINITY ? 0.f : p) + (m > -INFINITY ? 0.f : m);
 }
 
 template <int DV, int kW>
@@ -773,15 +769,44 @@ __global__ void __launch_bounds__(kJoin) cache_join_kernel(const Args a) {
     }
   }
   if (__any_sync(0xFFFFFFFFu, bad) && l == l) {
+    // The infinities of the parts' columns add up, and the keys of those that are NaN are looked
+    // at again: a long row's parts are many (131072 keys with one infinity: 0.3 ms, with a look
+    // at all of them 5.6).  With a warp per row at all keys of the two sets: the places of few
+    // and short parts are not worth the code (4096 sequences of 128 finite keys 682 us with it).
     const int64_t pitch = static_cast<int64_t>(a.HK) * DV;
     __syncwarp();  // (the warp's own stores are read back)
 #pragma unroll 1
     for (int d = warp * 32; d < DV; d += kW * 32) {
-      const int64_t at = static_cast<int64_t>(hk) * DV + d;
-      const float x = column_of_specials(a.v + b * a.S * pitch + at, clamped_len(a, b), a.vp + at,
-                                         a.P, pitch);
-      __nv_bfloat16* o = a.o + row * DV + d + 8 * (lane & 3) + (lane >> 2);
-      if (__hisnan(*o)) *o = __float2bfloat16(x);
+      const int col = d + 8 * (lane & 3) + (lane >> 2);
+      __nv_bfloat16* o = a.o + row * DV + col;
+      float sum = __hisnan(*o) ? 0.f : __uint_as_float(0x7FC00000u);  // (NaN: nothing to do)
+#pragma unroll 1
+      for (int i = 0; i < (kW > 1 ? n : 2) && __any_sync(0xFFFFFFFFu, sum == sum); ++i) {
+        const bool prefix = i < (kW > 1 ? n_p : 1);
+        const int64_t keys = prefix ? a.P : clamped_len(a, b);
+        int64_t j0 = 0, j1 = keys;
+        float x = __uint_as_float(0x7FC00000u);
+        if constexpr (kW > 1) {
+          if (ml_of(i)->y == 0.f) continue;
+          x = po_of(i)[col];
+          // the part's tiles: those that begin in its CTA's share of the line
+          const int wt = prefix ? a.wt_p : a.wt_c;
+          const int64_t at = prefix ? (static_cast<int64_t>(hk) * a.Rt + b / a.nb) *
+                                          length_of(a, a.Tp, a.wt_p)
+                                    : np + before * a.HK + hk * length_of(a, tb, a.wt_c);
+          const int64_t c = quotient64(at, q) + (prefix ? i : i - n_p);
+          j0 = quotient64(max64(c * q - at, 0) + wt - 1, wt) << a.kshift;
+          j1 = min64(quotient64((c + 1) * q - at + wt - 1, wt) << a.kshift, keys);
+        }
+        if (__any_sync(0xFFFFFFFFu, x != x && sum == sum)) {
+          const float y = column_of_specials(
+              (prefix ? a.vp : a.v + b * a.S * pitch) + j0 * pitch + hk * DV + d, j1 - j0, pitch);
+          if (x != x) x = y;
+        }
+        if (x - x != 0.f) sum += x;
+      }
+      // (none at all: finite values overflowed, and NaN stays)
+      if (__hisnan(*o) && sum != 0.f) *o = __float2bfloat16(sum);
     }
   }
   if (lane == 0 && warp == 0)

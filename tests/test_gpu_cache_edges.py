@@ -276,3 +276,60 @@ def test_rows_at_the_far_end_of_a_cache_of_more_than_2_to_the_32_elements():
         assert abs(lse[2, h, 0].item() - ref_lse.item()) <= ds
         tol = 2.0 ** -8 * (mag + ref.abs()) + (2 * ds + 2.0 ** -20) * mag
         assert ((o[2, 0, h].double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("shape", [dict(lens=[30001], P=0), dict(lens=[9, 2000, 777], P=5001),
+                                   dict(lens=[40 + i for i in range(600)], P=0),
+                                   dict(lens=[40 + i for i in range(600)], P=700)],
+                         ids=["one_long", "prefix", "many", "many_and_prefix"])
+@pytest.mark.parametrize("HQ", [4, 48], ids=["copies_of_rows", "wide_groups"])
+@pytest.mark.parametrize("D", [D64, D128, D192, D256], ids=str)
+def test_an_infinity_wherever_it_lies_is_found(D, HQ, shape):
+    """Every column of o has one infinite value, at a key of its own: in the first part of a row,
+    the last, beside the borders.  A quarter of the columns also have a NaN or the other infinity
+    elsewhere, whole rows of NaN come last."""
+    import torch
+    import index_sparse_attention_b200 as sa
+    g = torch.Generator(device="cuda")
+    g.manual_seed(17)
+    lens, P, Dv = shape["lens"], shape["P"], D[1]
+    B, S = len(lens), max(lens)
+    if B > 3 and HQ > 4:
+        HQ = 33
+    bf = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    q, k, v = bf(B, 1, HQ, D[0]), bf(B, S, 1, D[0]), bf(B, S, 1, Dv)
+    kp, vp = (bf(P, 1, D[0]), bf(P, 1, Dv)) if P else (None, None)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(18)
+    cols = torch.arange(Dv, device="cuda")
+    gpu = lambda x: torch.from_numpy(x.astype(np.float32)).cuda().bfloat16()
+    args = dict(q=q, k_cache=k, v_cache=v, lens=n, k_prefix=kp, v_prefix=vp)
+
+    def check():
+        """o is the sum of the infinities and NaN that a column's values hold, a number where they
+        hold none."""
+        live = torch.arange(S, device="cuda")[None] < n[:, None]
+        special = lambda x: torch.where(x.isfinite(), 0.0, x.double())
+        want = special(torch.where(live[..., None], v[:, :, 0], 0.0)).sum(1)
+        if P:
+            want = want + special(vp[:, 0]).sum(0)
+        o = sa.cache_attn_fwd(**args)[0][:, 0].double()
+        want = want[:, None].expand_as(o)
+        even = want == 0
+        assert o[even].isfinite().all()
+        assert torch.equal(o[~even].nan_to_num(7.0, 8.0, 9.0), want[~even].nan_to_num(7.0, 8.0, 9.0))
+
+    sign = np.where(rng.random(Dv) < 0.5, np.inf, -np.inf)
+    if P:  # the same for every sequence
+        vp[torch.from_numpy(rng.integers(0, P, Dv)).cuda(), 0, cols] = gpu(sign)
+    else:
+        for b in range(B):
+            v[b, torch.from_numpy(rng.integers(0, lens[b], Dv)).cuda(), 0, cols] = gpu(sign)
+    check()
+    other = np.where(rng.random(Dv) < 0.5, np.nan, -sign)[: Dv // 4]
+    v[:, min(lens) - 1, 0, :Dv // 4] = gpu(other)
+    if not P:  # (and an infinity that lay in the others' columns is gone)
+        v[:, min(lens) - 1, 0, Dv // 4:] = 0.0
+    check()
+    v[:, :min(lens)] = float("nan")
+    check()
