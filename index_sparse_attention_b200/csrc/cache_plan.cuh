@@ -2,17 +2,17 @@
 //
 // The work is a row of key tiles: first the prefix (for every KV head, every tile of query rows,
 // the P keys: all of one row tile before the next one's), then the caches (for every sequence,
-// every KV head, its own keys).  A run of tiles over one key set is a segment.  On a line a tile is as long as it takes (wt_p, wt_c) and
-// behind a segment's tiles lies a stretch `we` for what its end takes (reading O, joining its
-// row copies, the next rows' start).  CTA c takes the tiles that begin in [q c, q (c + 1)) of
-// that line (q: its length U over the number of CTAs), so that the CTAs end together whatever
-// the lengths are, and a segment that crosses a border is cut there.  (Counting tiles alone left
-// the CTA with the shortest sequences behind: 12 segments of one tile in its 15 tiles, 75000
-// cycles against 43000.)  q is at least the longer tile: then every CTA between a segment's
-// first and last one holds a part of it.  A part (segment s, CTA c) writes its un-normalised
-// output and its running max and sum to slot s + c: along the line each part has a larger s or a
-// larger c than the one before, so no two share a slot, and the joining kernel finds a segment's
-// parts from the same arithmetic.
+// every KV head, its own keys).  A run of tiles over one key set is a segment.  On a line a tile is
+// as long as it takes (wt_p, wt_c) and behind a segment's tiles lies a stretch `we` for what its
+// end takes (reading O, joining its row copies, the next rows' start).  CTA c takes the tiles that
+// begin in [q c, q (c + 1)) of that line (q: its length U over the number of CTAs), so that the
+// CTAs end together whatever the lengths are, and a segment that crosses a border is cut there.
+// (Counting tiles alone left the CTA with the shortest sequences behind: 12 segments of one tile in
+// its 15 tiles, 75000 cycles against 43000.)  q is at least the longer tile: then every CTA between
+// a segment's first and last one holds a part of it.  A part (segment s, CTA c) writes its un-
+// normalised output and its running max and sum to slot s + c: along the line each part has a
+// larger s or a larger c than the one before, so no two share a slot, and the joining kernel finds
+// a segment's parts from the same arithmetic.
 #pragma once
 
 #include <cuda_bf16.h>
