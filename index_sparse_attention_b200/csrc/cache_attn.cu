@@ -19,7 +19,7 @@
 // one TMA load), a row tile, so a prefix tile is read once for all of them.  More sequences make
 // more row tiles, each with its own pass over the prefix, and one that the L2 does not hold from
 // pass to pass comes from HBM each time (64 sequences of 4 heads a group over 32768 keys: two
-// passes, 134 of 1084 MB read).  A cache part holds the group's rows.
+// passes, 134 of 1098 MB read).  A cache part holds the group's rows.
 // An MMA has 128 rows: parts of up to 32 rows load their Q into all four lane quarters, and each
 // quarter's copy takes a quarter of the tile's keys (P is 0 elsewhere), so that all eight softmax
 // warps share the exponentials; the copies are added when the part ends.
